@@ -73,7 +73,15 @@ enum gqe_op {
   GQE_OP_DENSE = 6,
   GQE_OP_FORWARD_HOST = 7,
   GQE_OP_DECODE = 8,
-  GQE_OP_FORWARD_VARIANT = 9
+  GQE_OP_FORWARD_VARIANT = 9,
+  GQE_OP_TREE_ATTN = 10,
+  GQE_OP_CACHE_EVICT = 11
+};
+
+/* Which elements of a head gqe_qk_rope rotates as pair i < rot/2. */
+enum gqe_rope_layout {
+  GQE_ROPE_HALF = 0,        /* i and i + rot/2  */
+  GQE_ROPE_INTERLEAVED = 1  /* 2 i and 2 i + 1  */
 };
 
 /* Output construction of gqe_forward_variant. */
@@ -335,6 +343,141 @@ int gqe_decode(const gqe_dims* d, const int32_t* cache_len, const void* x_new,
 int gqa_dense_forward(const gqe_dims* d, const void* x, const void* Wq,
                       const void* Wk, const void* Wv, const void* Wo_dense,
                       void* y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Serving with drafted tokens: gqe_qk_rope, gqe_tree_attn, gqe_tree_commit and
+ * gqe_cache_evict are the steps around the key/value cache that the layer's own
+ * stages leave open. One step of a server that drafts T tokens for each of B
+ * sequences runs, with ONE gqe_dims of that B and T,
+ *     gqe_route, gqe_qproj   on the drafted tokens          -> sel, w, Q, K, V
+ *     gqe_qk_rope            norms and rotation             -> Q, K
+ *     gqe_tree_attn          over the cache and the drafts  -> O, lse
+ *     gqe_combine                                           -> y
+ * and, once it knows which drafts are accepted, gqe_tree_commit, and from time
+ * to time gqe_cache_evict. T = 1 without a tree is a plain generation step; a
+ * prompt goes in chunks of up to 128 tokens. (The method's pages describe
+ * neither positions nor drafts nor eviction: these entry points are the
+ * library's own.)
+ *
+ * The cache of a layer: K_cache, V_cache [B, cap, G, dh] bf16, rows
+ * s < cache_len[b] in use; mass [B, G, cap] fp32, the attention weight that
+ * each position has received; pos [B, G, cap] int32, the position of the token
+ * that each row holds (a group's rows stay in any order once some were
+ * evicted). Rows at and past cache_len[b] are never used, whatever they hold.
+ *
+ * A length, index or expert out of range that only the device sees sets the
+ * device check word (gqe_check_error returns GQE_ERR_DEVICE_CHECK) and the
+ * sequence, or row, that it belongs to is skipped.
+ */
+
+/*
+ * gqe_qk_rope -- the norms of queries and keys of each head and the rotation
+ * by position, in one pass.
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        per head of 64
+ *   (a, b) -> (a c - b s, b c + a s)               per pair i < rot/2
+ *   c = scale * cos(pos * inv_freq[i]), s = scale * sin(pos * inv_freq[i])
+ * Elements rot..63 are not rotated. Arithmetic in fp32, the result rounded
+ * once; the angles are reduced in fp64, exact at any int32 position.
+ *
+ * layout : enum gqe_rope_layout; rot even, 0..64 (0: the norms alone).
+ * scale  : 1, or the attention factor of a frequency scaling that has one.
+ * In : Q [B*T, G*k+1, 64], K [B*T, G, 64] bf16 (either may be NULL with its
+ *      output: that side is left out);
+ *      wq [G*M+1, 64] bf16, a row for each routed head h = g*M + e and the
+ *      last for the shared head; the row of slot (n, g, j) is that of expert
+ *      sel[n, g, j]. wk [G, 64] bf16. A NULL weight leaves that side's norm out;
+ *      sel [B*T, G, k] int32 from gqe_route (needed with wq; k = M: 0..M-1);
+ *      inv_freq [rot/2] fp32 (NULL with rot = 0);
+ *      positions [B*T] int32, or NULL: token t of a sequence is at t.
+ * Out: Qo, Ko, as Q and K; they may be Q and K themselves.
+ * ws : none. An expert outside [0, M) is recorded; its row is undefined.
+ */
+int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale,
+                const void* Q, const void* K, const void* wq, const void* wk,
+                const int32_t* sel, const float* inv_freq,
+                const int32_t* positions, void* Qo, void* Ko, void* stream);
+
+/*
+ * gqe_tree_attn -- attention of drafted tokens over a cache. Token i of
+ * sequence b (i < draft_len[b] <= T) attends the cached rows s < cache_len[b],
+ * itself and its ancestors in the draft tree; the shared head attends KV
+ * head 0. T <= 128.
+ *
+ * In : Q [B*T, G*k+1, 64], K_new, V_new [B*T, G, 64] bf16: the drafted tokens;
+ *      K_cache, V_cache [B, cap, G, 64] bf16; cache_len [B] int32 in [0, cap];
+ *      draft_len [B] int32 in [0, T], or NULL: T each;
+ *      parent [B*T] int32: the parent of token i, parent < i, or -1 for a
+ *      child of the cached sequence; NULL: a chain, parent[i] = i - 1. A
+ *      parent that is neither is recorded and taken as -1.
+ * Out: O [B*T, G*k+1, 64] bf16; lse [B*T, G*k+1] fp32, log sum_s exp(q.k_s / 8)
+ *      over the attended rows, or NULL. Rows i >= draft_len[b] are left as they
+ *      were.
+ * What a masked row holds never reaches a result, infinities and NaN included.
+ * Arithmetic: S, l and O accumulate in fp32, P rounded to bf16 before P V.
+ * ws : gqe_workspace_bytes(d, GQE_OP_TREE_ATTN); it does not grow with cap.
+ * The result does not change from call to call (no atomics). B*cap < 2^31.
+ */
+int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q,
+                  const void* K_new, const void* V_new, const void* K_cache,
+                  const void* V_cache, const int32_t* cache_len,
+                  const int32_t* draft_len, const int32_t* parent, void* O,
+                  float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gqe_tree_commit -- the accepted drafts of every sequence appended to the
+ * cache, and their attention weight added to the positions' sums.
+ * The accepted tokens of sequence b are path[b, 0 .. n-1], n = n_acc[b], in
+ * order from the cached sequence on, each the child of the one before. Token
+ * path[b, j] goes to row L + j, L = cache_len[b], and
+ *   mass_out[b, g, s] = mass_in[b, g, s] (0 for s >= L)
+ *      + sum over j with s <= L + j, and over the group's query rows (k, and
+ *        the shared head's in group 0), of exp(q.k_s / 8 - lse)
+ * for every s < L + n, which adds up to one for each query row.
+ *
+ * In : path [B, T] int32 in [0, T), or NULL: 0, 1, 2, ...; n_acc [B] int32 in
+ *      [0, T], or NULL: T each; L + n <= cap;
+ *      positions [B*T] int32 of the drafted tokens, or NULL: row L + j is at
+ *      position L + j; Q, K_new, V_new and lse of the gqe_tree_attn call;
+ *      cache_len [B] int32.
+ * In/out: K_cache, V_cache [B, cap, G, 64]: rows L .. L+n-1 are written;
+ *      pos [B, G, cap], or NULL: the same entries.
+ * Out: mass_out [B, G, cap] fp32, entries below L + n; it may be mass_in.
+ *      Both NULL: the weights are not accumulated, Q and lse are not read.
+ *      new_len [B] = L + n; not cache_len itself.
+ * ws : none.
+ */
+int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path,
+                    const int32_t* n_acc, const int32_t* positions,
+                    const void* Q, const float* lse, const void* K_new,
+                    const void* V_new, const int32_t* cache_len, void* K_cache,
+                    void* V_cache, int32_t* pos, const float* mass_in,
+                    float* mass_out, int32_t* new_len, void* stream);
+
+/*
+ * gqe_cache_evict -- eviction by accumulated attention weight. In every
+ * (sequence, group) with more than `keep` rows in use, `keep` of them stay:
+ *   - rows of a position below `sink`, or of one of the last `recent`
+ *     positions (pos >= next_pos[b] - recent);
+ *   - then those with the largest mass, ties to the lower row, NaN last.
+ * The rows that stay at or past row `keep` move into the rows below it that
+ * were left, both in ascending order; no other row moves (attention does not
+ * depend on the order of rows). d->T is the cache's capacity here.
+ *
+ * In : keep >= 1; sink, recent >= 0, sink + recent <= keep; cache_len [B]
+ *      int32 in [0, d->T]; next_pos [B] int32: the position of the sequence's
+ *      next token; mass_in [B, G, T] fp32; pos_in [B, G, T] int32.
+ * In/out: K_cache, V_cache [B, T, G, 64] bf16.
+ * Out: mass_out, pos_out: the entries of the rows below new_len; they may be
+ *      mass_in and pos_in. new_len [B] = min(cache_len, keep); not cache_len
+ *      itself.
+ * ws : gqe_workspace_bytes(d, GQE_OP_CACHE_EVICT).
+ */
+int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink,
+                    int32_t recent, const int32_t* cache_len,
+                    const int32_t* next_pos, void* K_cache, void* V_cache,
+                    const float* mass_in, float* mass_out,
+                    const int32_t* pos_in, int32_t* pos_out, int32_t* new_len,
+                    void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read and clear the current device's sticky
  * error word: GQE_OK, GQE_ERR_TIMEOUT, GQE_ERR_DEVICE_CHECK, or GQE_ERR_CUDA

@@ -7,6 +7,8 @@ with the C ABI's entry-point names.
 from . import lib  # noqa: F401
 from .lib import (  # noqa: F401
     gqe_route, gqe_qproj, gqe_attn, gqe_combine, gqe_forward, gqe_forward_variant, gqe_forward_host, gqe_decode,
+    gqe_qk_rope, rope_frequencies, gqe_tree_attn, gqe_tree_commit, gqe_cache_evict, ROPE_HALF, ROPE_INTERLEAVED,
+    OP_TREE_ATTN, OP_CACHE_EVICT,
     gqa_dense_forward, COMBINE_SLOT, COMBINE_HARD, COMBINE_WEIGHTED, COMBINE_GLOBAL_SLOT, COMBINE_NO_SHARED,
     QPROJ_AUTO, QPROJ_GATHER, QPROJ_DENSE,
     OP_FORWARD_VARIANT,

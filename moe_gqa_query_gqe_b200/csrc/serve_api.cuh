@@ -1,0 +1,245 @@
+// serve_api.cuh -- C entry points of the operators around the key/value cache
+// (declared in include/gqe.h): argument checks, workspace and launches. Part
+// of gqe_api.cu's translation unit.
+#pragma once
+
+#include "cache.cuh"
+#include "rope.cuh"
+#include "tree.cuh"
+
+namespace {
+
+int check_opt(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p != nullptr && !aligned16(p)) return GQE_ERR_INVALID_ARG;
+  return GQE_OK;
+}
+
+// Row tiles and key splits of the tree attention. The split does not depend on
+// the cache's capacity (nor does the workspace): enough blocks to fill the GPU.
+struct TreePlan {
+  int wr, rows, ntile0, nrt, units, nsplit;
+};
+constexpr int kTreeBlocks = 148 * 4;
+TreePlan tree_plan(const gqe_dims* d) {
+  TreePlan t;
+  const int R = d->T * d->k;
+  t.wr = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
+  t.rows = 16 * t.wr;
+  t.ntile0 = (int)cdiv(R + d->T, t.rows);
+  t.nrt = (int)cdiv(R, t.rows);
+  t.units = d->B * (t.ntile0 + (d->G - 1) * t.nrt);
+  t.nsplit = (int)std::max<long long>(1, cdiv(kTreeBlocks, t.units));
+  return t;
+}
+size_t tree_ws_bytes(const gqe_dims* d, float** ml, float** o, uint8_t* ws) {
+  const TreePlan t = tree_plan(d);
+  Carver c{ws};
+  const size_t parts = t.nsplit > 1 ? (size_t)t.units * t.nsplit * t.rows : 0;
+  float* a = c.take<float>(parts * 2);
+  float* b = c.take<float>(parts * 64);
+  if (ml) *ml = a;
+  if (o) *o = b;
+  return c.off;
+}
+
+// Sequences, drafted tokens and capacity of the cache operators.
+int check_tree_dims(const gqe_dims* d, int cap) {
+  GQE_TRY(check_dims(d));
+  if (cap < 1) return GQE_ERR_INVALID_ARG;
+  if (d->T > kTreeMax || (long long)d->B * cap >= (1ll << 31)) return GQE_ERR_UNSUPPORTED;
+  return GQE_OK;
+}
+
+int evict_list(const gqe_dims* d) { return d->T / 2 + 1; }
+size_t evict_ws_bytes(const gqe_dims* d, EvictParams* p, uint8_t* ws) {
+  Carver c{ws};
+  const size_t bg = (size_t)d->B * d->G;
+  int32_t* moves = c.take<int32_t>(bg);
+  int32_t* holes = c.take<int32_t>(bg * evict_list(d));
+  int32_t* late = c.take<int32_t>(bg * evict_list(d));
+  if (p) {
+    p->moves = moves;
+    p->holes = holes;
+    p->late = late;
+  }
+  return c.off;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale, const void* Q, const void* K,
+                const void* wq, const void* wk, const int32_t* sel, const float* inv_freq, const int32_t* positions,
+                void* Qo, void* Ko, void* stream) {
+  GQE_TRY(check_dims(d));
+  if (layout != GQE_ROPE_HALF && layout != GQE_ROPE_INTERLEAVED) return GQE_ERR_INVALID_ARG;
+  if (rot < 0 || rot > 64 || (rot & 1) != 0 || !(eps >= 0.f)) return GQE_ERR_INVALID_ARG;
+  if ((Q == nullptr) != (Qo == nullptr) || (K == nullptr) != (Ko == nullptr)) return GQE_ERR_INVALID_ARG;
+  if (Q == nullptr && K == nullptr) return GQE_ERR_INVALID_ARG;
+  if (Q != nullptr && wq != nullptr && sel == nullptr) return GQE_ERR_INVALID_ARG;
+  if (rot > 0 && inv_freq == nullptr) return GQE_ERR_INVALID_ARG;
+  GQE_TRY(check_opt({Q, K, wq, wk, sel, inv_freq, positions, Qo, Ko}));
+  GQE_TRY(check_device());
+  RopeParams p;
+  memset(&p, 0, sizeof(p));
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.K = static_cast<const __nv_bfloat16*>(K);
+  p.wq = static_cast<const __nv_bfloat16*>(wq);
+  p.wk = static_cast<const __nv_bfloat16*>(wk);
+  p.sel = sel;
+  p.inv_freq = inv_freq;
+  p.positions = positions;
+  p.Qo = static_cast<__nv_bfloat16*>(Qo);
+  p.Ko = static_cast<__nv_bfloat16*>(Ko);
+  p.eps = eps;
+  p.scale = scale;
+  p.N = d->B * d->T;
+  p.T = d->T;
+  p.G = d->G;
+  p.M = d->M;
+  p.k = d->k;
+  p.Ha = d->G * d->k + 1;
+  p.Hq = Q ? p.Ha : 0;
+  p.Hk = K ? d->G : 0;
+  p.rot = rot;
+  // about 128 head rows (four passes) a block, fewer tokens while that leaves
+  // SMs without a block
+  const int H = p.Hq + p.Hk;
+  p.tpb = std::min(kRopeMaxTpb, std::max(1, 128 / H));
+  while (p.tpb > 1 && cdiv(p.N, p.tpb) < sm_count()) p.tpb /= 2;
+  const dim3 grid((unsigned)cdiv(p.N, p.tpb));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (layout == GQE_ROPE_INTERLEAVED || rot == 0)
+    return launch_pdl(qk_rope_kernel<kRopeInterleaved>, grid, dim3(kRopeThreads), 0, st, p);
+  if (rot % 16 == 0) return launch_pdl(qk_rope_kernel<kRopeHalf8>, grid, dim3(kRopeThreads), 0, st, p);
+  return launch_pdl(qk_rope_kernel<kRopeHalfAny>, grid, dim3(kRopeThreads), 0, st, p);
+}
+
+int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_new, const void* V_new,
+                  const void* K_cache, const void* V_cache, const int32_t* cache_len, const int32_t* draft_len,
+                  const int32_t* parent, void* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  GQE_TRY(check_tree_dims(d, cap));
+  GQE_TRY(check_ptrs({Q, K_new, V_new, K_cache, V_cache, cache_len, O}));
+  GQE_TRY(check_opt({draft_len, parent, lse}));
+  GQE_TRY(check_ws(ws, ws_bytes, gqe_workspace_bytes(d, GQE_OP_TREE_ATTN)));
+  GQE_TRY(check_device());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const TreePlan t = tree_plan(d);
+  TreeParams p;
+  memset(&p, 0, sizeof(p));
+  tree_ws_bytes(d, &p.part_ml, &p.part_o, static_cast<uint8_t*>(ws));
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.Kn = static_cast<const __nv_bfloat16*>(K_new);
+  p.Vn = static_cast<const __nv_bfloat16*>(V_new);
+  p.Kc = static_cast<const __nv_bfloat16*>(K_cache);
+  p.Vc = static_cast<const __nv_bfloat16*>(V_cache);
+  p.cache_len = cache_len;
+  p.draft_len = draft_len;
+  p.parent = parent;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.lse = lse;
+  p.B = d->B;
+  p.T = d->T;
+  p.G = d->G;
+  p.k = d->k;
+  p.Ha = d->G * d->k + 1;
+  p.cap = cap;
+  p.ntile0 = t.ntile0;
+  p.nrt = t.nrt;
+  // no more splits than blocks of keys
+  p.nsplit = (int)std::min<long long>(t.nsplit, cdiv(cap, kTmKeys) + cdiv(d->T, kTmKeys));
+  p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
+  const dim3 grid((unsigned)(t.units * p.nsplit));
+  auto run = [&](auto kern) -> int {
+    GQE_TRY(set_smem(kern, kTmSmem));
+    return launch_pdl(kern, grid, dim3(kTmThreads), kTmSmem, st, p);
+  };
+  GQE_TRY(t.wr == 1 ? run(tree_attn_mma_kernel<1>) : (t.wr == 2 ? run(tree_attn_mma_kernel<2>) : run(tree_attn_mma_kernel<4>)));
+  if (p.nsplit == 1) return GQE_OK;
+  const long long rows = (long long)d->B * d->T * p.Ha;
+  return launch_pdl(tree_merge_kernel, dim3((unsigned)cdiv(rows, kTreeMergeThreads / 32)), dim3(kTreeMergeThreads), 0, st, p,
+                    t.rows);
+}
+
+int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path, const int32_t* n_acc, const int32_t* positions,
+                    const void* Q, const float* lse, const void* K_new, const void* V_new, const int32_t* cache_len,
+                    void* K_cache, void* V_cache, int32_t* pos, const float* mass_in, float* mass_out, int32_t* new_len,
+                    void* stream) {
+  GQE_TRY(check_tree_dims(d, cap));
+  GQE_TRY(check_ptrs({K_new, V_new, cache_len, K_cache, V_cache, new_len}));
+  GQE_TRY(check_opt({path, n_acc, positions, Q, lse, pos, mass_in, mass_out}));
+  if ((mass_in == nullptr) != (mass_out == nullptr)) return GQE_ERR_INVALID_ARG;
+  if (mass_in != nullptr && (Q == nullptr || lse == nullptr)) return GQE_ERR_INVALID_ARG;
+  if (new_len == cache_len) return GQE_ERR_INVALID_ARG;
+  GQE_TRY(check_device());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CommitParams p;
+  memset(&p, 0, sizeof(p));
+  p.path = path;
+  p.n_acc = n_acc;
+  p.positions = positions;
+  p.cache_len = cache_len;
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.lse = lse;
+  p.Kn = static_cast<const __nv_bfloat16*>(K_new);
+  p.Vn = static_cast<const __nv_bfloat16*>(V_new);
+  p.Kc = static_cast<__nv_bfloat16*>(K_cache);
+  p.Vc = static_cast<__nv_bfloat16*>(V_cache);
+  p.pos = pos;
+  p.mass_in = mass_in;
+  p.mass_out = mass_out;
+  p.new_len = new_len;
+  p.B = d->B;
+  p.T = d->T;
+  p.G = d->G;
+  p.k = d->k;
+  p.Ha = d->G * d->k + 1;
+  p.cap = cap;
+  p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
+  GQE_TRY(launch_pdl(commit_append_kernel, dim3((unsigned)(d->B * d->T)), dim3(kAppendThreads), 0, st, p));
+  if (mass_in == nullptr) return GQE_OK;
+  const long long bg = (long long)d->B * d->G;
+  p.nsplit = (int)std::min<long long>(cdiv(cap, kMassKeys), std::max<long long>(1, cdiv(148 * 8, bg)));
+  return launch_pdl(cache_mass_mma_kernel, dim3((unsigned)(bg * p.nsplit)), dim3(kMassThreads), 0, st, p);
+}
+
+int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink, int32_t recent, const int32_t* cache_len,
+                    const int32_t* next_pos, void* K_cache, void* V_cache, const float* mass_in, float* mass_out,
+                    const int32_t* pos_in, int32_t* pos_out, int32_t* new_len, void* ws, size_t ws_bytes,
+                    void* stream) {
+  GQE_TRY(check_dims(d));
+  if (keep < 1 || sink < 0 || recent < 0 || (long long)sink + recent > keep) return GQE_ERR_INVALID_ARG;
+  GQE_TRY(check_ptrs({cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out, new_len}));
+  if (new_len == cache_len) return GQE_ERR_INVALID_ARG;
+  GQE_TRY(check_ws(ws, ws_bytes, gqe_workspace_bytes(d, GQE_OP_CACHE_EVICT)));
+  GQE_TRY(check_device());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  EvictParams p;
+  memset(&p, 0, sizeof(p));
+  evict_ws_bytes(d, &p, static_cast<uint8_t*>(ws));
+  p.cache_len = cache_len;
+  p.next_pos = next_pos;
+  p.Kc = static_cast<__nv_bfloat16*>(K_cache);
+  p.Vc = static_cast<__nv_bfloat16*>(V_cache);
+  p.mass_in = mass_in;
+  p.mass_out = mass_out;
+  p.pos_in = pos_in;
+  p.pos_out = pos_out;
+  p.new_len = new_len;
+  p.B = d->B;
+  p.G = d->G;
+  p.cap = d->T;
+  p.keep = keep;
+  p.sink = sink;
+  p.recent = recent;
+  p.list = evict_list(d);
+  const long long bg = (long long)d->B * d->G;
+  GQE_TRY(launch_pdl(evict_select_kernel, dim3((unsigned)bg), dim3(kEvictThreads), 0, st, p));
+  const long long most = std::max<long long>(1, std::min<long long>(keep, d->T / 2 + 1));
+  const long long blocks = std::min<long long>(cdiv(most, kMoveThreads / 8), std::max<long long>(1, cdiv(148 * 8, bg)));
+  return launch_pdl(evict_move_kernel, dim3((unsigned)blocks, (unsigned)bg), dim3(kMoveThreads), 0, st, p);
+}
+
+}  // extern "C"

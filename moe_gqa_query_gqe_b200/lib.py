@@ -20,13 +20,17 @@ STATUS = {0: "GQE_OK", -1: "GQE_ERR_INVALID_ARG", -2: "GQE_ERR_UNSUPPORTED", -3:
           -7: "GQE_ERR_DEVICE_CHECK"}
 OP_ROUTE, OP_QPROJ, OP_ATTN, OP_COMBINE, OP_FORWARD, OP_DENSE, OP_FORWARD_HOST, OP_DECODE, OP_FORWARD_VARIANT = \
     1, 2, 3, 4, 5, 6, 7, 8, 9
+OP_TREE_ATTN, OP_CACHE_EVICT = 10, 11
 COMBINE_SLOT, COMBINE_HARD, COMBINE_WEIGHTED, COMBINE_GLOBAL_SLOT, COMBINE_NO_SHARED = 0, 1, 2, 3, 4
 # selected-query path of gqe_forward_variant, or'ed into the mode (enum gqe_qproj_path)
 QPROJ_AUTO, QPROJ_GATHER, QPROJ_DENSE = 0, 0x100, 0x200
+# pairs of gqe_qk_rope (enum gqe_rope_layout)
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 
 # every symbol include/gqe.h declares
 EXPORTS = ("gqe_workspace_bytes", "gqe_validate_dims", "gqe_route", "gqe_route_noalloc", "gqe_qproj", "gqe_attn", "gqe_combine",
-           "gqe_forward", "gqe_forward_variant", "gqe_forward_host", "gqe_decode", "gqa_dense_forward", "gqe_check_error", "gqe_status_string", "gqe_last_cuda_error",
+           "gqe_forward", "gqe_forward_variant", "gqe_forward_host", "gqe_decode", "gqa_dense_forward",
+           "gqe_qk_rope", "gqe_tree_attn", "gqe_tree_commit", "gqe_cache_evict", "gqe_check_error", "gqe_status_string", "gqe_last_cuda_error",
            "gqe_selftest_wait_timeout", "gqe_version")
 
 
@@ -66,6 +70,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gqe_forward_variant": (ctypes.c_int, [dp, ctypes.c_int, vp, vp, vp, vp, vp, f32p, vp, vp, vp, sz, vp]),
         "gqe_forward_host": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, f32p, vp, vp, vp, sz, vp]),
         "gqa_dense_forward": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "gqe_qk_rope": (ctypes.c_int, [dp, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_float, vp, vp, vp, vp, i32p,
+                                       f32p, i32p, vp, vp, vp]),
+        "gqe_tree_attn": (ctypes.c_int, [dp, ctypes.c_int32, vp, vp, vp, vp, vp, i32p, i32p, i32p, vp, f32p, vp, sz, vp]),
+        "gqe_tree_commit": (ctypes.c_int, [dp, ctypes.c_int32, i32p, i32p, i32p, vp, f32p, vp, vp, i32p, vp, vp, i32p, f32p,
+                                           f32p, i32p, vp]),
+        "gqe_cache_evict": (ctypes.c_int, [dp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, i32p, i32p, vp, vp, f32p,
+                                           f32p, i32p, i32p, i32p, vp, sz, vp]),
         "gqe_check_error": (ctypes.c_int, [vp]),
         "gqe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "gqe_last_cuda_error": (ctypes.c_char_p, []),
@@ -184,6 +195,165 @@ def gqe_forward_host(dims, x_host, Wq, Wk, Wv, Wr, br, Wo, y_host, ws, stream=No
 def gqa_dense_forward(dims, x, Wq, Wk, Wv, Wo_dense, y, ws, stream=None) -> None:
     _call("gqa_dense_forward", ctypes.byref(dims_struct(dims)), _ptr(x), _ptr(Wq), _ptr(Wk), _ptr(Wv),
           _ptr(Wo_dense), _ptr(y), _ptr(ws), ws.numel(), _stream(stream))
+
+
+# ---- operators around the key/value cache ----------------------------------------
+# Their tensors are checked here, before the call: each is contiguous, on the
+# current device, of the stated type and of as many elements as the dimensions
+# say. A tensor that is not raises GqeError (GQE_ERR_INVALID_ARG) and names it.
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _checked(fn: str, device: int, specs) -> list:
+    """Data pointers of (name, tensor, dtype, elements, needed) in order; None
+    stays None where it is not needed."""
+    out = []
+    for name, t, dtype, n, needed in specs:
+        if t is None:
+            if needed:
+                raise GqeError(fn, -1, f"{name} is missing")
+            out.append(None)
+            continue
+        if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+            raise GqeError(fn, -1, f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{device}, got "
+                                   f"{tuple(t.shape)} {t.dtype} on {t.device}"
+                                   f"{'' if t.is_contiguous() else ', not contiguous'}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _bytes(ws) -> int:
+    return 0 if ws is None else ws.numel()
+
+
+def _run(fn: str, device: int, stream, *args) -> None:
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)  # current_stream() without its Python object
+    _call(fn, *args, _stream(stream))
+
+
+def _device(fn: str) -> int:
+    if not torch.cuda.is_available():
+        raise GqeError(fn, -6)
+    return torch.cuda.current_device()
+
+
+def gqe_qk_rope(dims, Q, K, wq, wk, sel, inv_freq, positions, Qo, Ko, *, layout=ROPE_HALF, rot=64, eps=1e-6, scale=1.0,
+                stream=None) -> None:
+    """Norms of the queries and keys of each head and the rotation by position
+    in one pass: Q [B*T, G*k+1, 64] and K [B*T, G, 64] to Qo and Ko (which may
+    be Q and K). wq [G*M+1, 64], chosen by sel, and wk [G, 64] are the norms'
+    weights, or None without a norm; inv_freq [rot/2] and scale come from
+    rope_frequencies; positions [B*T], or None for 0..T-1 in each sequence.
+    Either of Q and K may be None together with its output."""
+    d = dims_struct(dims)
+    fn, dev = "gqe_qk_rope", _device("gqe_qk_rope")
+    N, q, k = d.B * d.T, d.B * d.T * (d.G * d.k + 1) * 64, d.B * d.T * d.G * 64
+    need_q, need_k = Q is not None or Qo is not None, K is not None or Ko is not None
+    p = _checked(fn, dev, (("Q", Q, _BF16, q, need_q), ("K", K, _BF16, k, need_k), ("wq", wq, _BF16, (d.G * d.M + 1) * 64, False),
+                           ("wk", wk, _BF16, d.G * 64, False),
+                           ("sel", sel, _I32, N * d.G * d.k, wq is not None and Q is not None),
+                           ("inv_freq", inv_freq if rot else None, _F32, rot // 2, rot != 0), ("positions", positions, _I32, N, False),
+                           ("Qo", Qo, _BF16, q, need_q), ("Ko", Ko, _BF16, k, need_k)))
+    _run(fn, dev, stream, ctypes.byref(d), layout, rot, eps, scale, *p)
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0,
+                     device=None):
+    """(inv_freq, scale) of gqe_qk_rope: pair i < rot/2 turns by
+    base^(-2 i / rot) radians a position, stretched for contexts `factor` times
+    as long as the trained one by
+      scaling=None      nothing (factor is not used)
+      scaling="linear"  every frequency over `factor`
+      scaling="ntk"     the base raised, base * factor^(rot / (rot - 2)): the
+                        slowest pair is stretched by `factor`, the fastest not
+      scaling="yarn"    pairs with more than beta_fast turns in trained_len
+                        positions kept, those with fewer than beta_slow over
+                        `factor`, a linear ramp (over the pair's index) between;
+                        scale = 0.1 ln(factor) + 1
+    Computed in fp64, rounded to fp32 once."""
+    import math
+    if rot < 2 or rot > 64 or rot % 2:
+        raise ValueError(f"rot must be even, 2..64, got {rot}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError(f"base must be above 1 and factor at least 1, got {base}, {factor}")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot == 2:
+            raise ValueError("ntk scaling needs rot > 2")
+        base = base * factor ** (rot / (rot - 2))
+    inv, scale = base ** (-2.0 * i / rot), 1.0
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        if trained_len < 1:
+            raise ValueError("yarn scaling needs trained_len")
+        # index of the pair that makes `turns` turns in trained_len positions
+        def at(turns):
+            return rot * math.log(trained_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+        lo, hi = max(math.floor(at(beta_fast)), 0), min(math.ceil(at(beta_slow)), rot // 2 - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        inv = inv * (1.0 - ramp) + inv / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    return inv.float().to(device or "cuda"), scale
+
+
+def gqe_tree_attn(dims, cap, Q, K_new, V_new, K_cache, V_cache, cache_len, draft_len, parent, O, lse, ws, *,
+                  stream=None) -> None:
+    """Attention of T drafted tokens a sequence (dims.T <= 128) over the first
+    cache_len[b] rows of caches [B, cap, G, 64], themselves and their ancestors:
+    parent [B*T] (None: a chain). draft_len [B] (None: T each). Writes O
+    [B*T, G*k+1, 64] and lse [B*T, G*k+1] (or None)."""
+    d = dims_struct(dims)
+    fn, dev = "gqe_tree_attn", _device("gqe_tree_attn")
+    N, Ha = d.B * d.T, d.G * d.k + 1
+    kn, kc = N * d.G * 64, d.B * cap * d.G * 64
+    p = _checked(fn, dev, (("Q", Q, _BF16, N * Ha * 64, True), ("K_new", K_new, _BF16, kn, True), ("V_new", V_new, _BF16, kn, True),
+                           ("K_cache", K_cache, _BF16, kc, True), ("V_cache", V_cache, _BF16, kc, True),
+                           ("cache_len", cache_len, _I32, d.B, True), ("draft_len", draft_len, _I32, d.B, False),
+                           ("parent", parent, _I32, N, False), ("O", O, _BF16, N * Ha * 64, True),
+                           ("lse", lse, _F32, N * Ha, False), ("ws", ws, torch.uint8, _bytes(ws), True)))
+    _run(fn, dev, stream, ctypes.byref(d), cap, *p, _bytes(ws))
+
+
+def gqe_tree_commit(dims, cap, path, n_acc, positions, Q, lse, K_new, V_new, cache_len, K_cache, V_cache, pos, mass_in,
+                    mass_out, new_len, *, stream=None) -> None:
+    """Appends the accepted drafts path[b, :n_acc[b]] to the caches and adds
+    their attention weight to the positions' sums: mass [B, G, cap] (both None:
+    not accumulated), pos [B, G, cap] (or None). mass_out may be mass_in;
+    new_len may not be cache_len."""
+    d = dims_struct(dims)
+    fn, dev = "gqe_tree_commit", _device("gqe_tree_commit")
+    N, Ha = d.B * d.T, d.G * d.k + 1
+    kn, kc, rows = N * d.G * 64, d.B * cap * d.G * 64, d.B * d.G * cap
+    m = mass_in is not None or mass_out is not None
+    p = _checked(fn, dev, (("path", path, _I32, N, False), ("n_acc", n_acc, _I32, d.B, False), ("positions", positions, _I32, N, False),
+                           ("Q", Q, _BF16, N * Ha * 64, m), ("lse", lse, _F32, N * Ha, m), ("K_new", K_new, _BF16, kn, True),
+                           ("V_new", V_new, _BF16, kn, True), ("cache_len", cache_len, _I32, d.B, True),
+                           ("K_cache", K_cache, _BF16, kc, True), ("V_cache", V_cache, _BF16, kc, True),
+                           ("pos", pos, _I32, rows, False), ("mass_in", mass_in, _F32, rows, m), ("mass_out", mass_out, _F32, rows, m),
+                           ("new_len", new_len, _I32, d.B, True)))
+    _run(fn, dev, stream, ctypes.byref(d), cap, *p)
+
+
+def gqe_cache_evict(dims, keep, sink, recent, cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out,
+                    new_len, ws, *, stream=None) -> None:
+    """Keeps `keep` rows of every (sequence, group) of caches [B, T, G, 64]
+    (dims.T: their capacity): positions below `sink` and the last `recent`,
+    then the largest mass; the cache is closed up in place. mass_out and
+    pos_out may be mass_in and pos_in; new_len may not be cache_len."""
+    d = dims_struct(dims)
+    fn, dev = "gqe_cache_evict", _device("gqe_cache_evict")
+    kc, rows = d.B * d.T * d.G * 64, d.B * d.G * d.T
+    p = _checked(fn, dev, (("cache_len", cache_len, _I32, d.B, True), ("next_pos", next_pos, _I32, d.B, True),
+                           ("K_cache", K_cache, _BF16, kc, True), ("V_cache", V_cache, _BF16, kc, True),
+                           ("mass_in", mass_in, _F32, rows, True), ("mass_out", mass_out, _F32, rows, True),
+                           ("pos_in", pos_in, _I32, rows, True), ("pos_out", pos_out, _I32, rows, True),
+                           ("new_len", new_len, _I32, d.B, True), ("ws", ws, torch.uint8, _bytes(ws), True)))
+    _run(fn, dev, stream, ctypes.byref(d), keep, sink, recent, *p, _bytes(ws))
 
 
 def gqe_check_error(stream=None) -> int:
