@@ -104,10 +104,12 @@ int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale, 
   p.Hq = Q ? p.Ha : 0;
   p.Hk = K ? d->G : 0;
   p.rot = rot;
-  // about 128 head rows (four passes) a block, fewer tokens while that leaves
+  for (p.log2k = 0; (1 << p.log2k) < d->k;) ++p.log2k;
+  // about 256 head rows (four passes) a block, fewer tokens while that leaves
   // SMs without a block
   const int H = p.Hq + p.Hk;
-  p.tpb = std::min(kRopeMaxTpb, std::max(1, 128 / H));
+  p.inv_H = ((1u << 20) + H - 1) / H;
+  p.tpb = std::min(kRopeMaxTpb, std::max(1, 256 / H));
   while (p.tpb > 1 && cdiv(p.N, p.tpb) < sm_count()) p.tpb /= 2;
   const dim3 grid((unsigned)cdiv(p.N, p.tpb));
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -94,6 +94,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 def dims_struct(d) -> GqeDims:
     if isinstance(d, GqeDims):
         return d
+    if type(d) is dict:
+        return GqeDims(d["B"], d["T"], d["D"], d["G"], d["M"], d["k"], d["dh"])
     get = (lambda n: d[n]) if isinstance(d, dict) else (lambda n: getattr(d, n))
     return GqeDims(*(int(get(n)) for n in ("B", "T", "D", "G", "M", "k", "dh")))
 
@@ -115,7 +117,7 @@ def _stream(stream) -> int:
 
 
 def _call(name: str, *args) -> None:
-    code = getattr(load(), name)(*args)
+    code = getattr(_lib or load(), name)(*args)
     if code != GQE_OK:
         detail = load().gqe_last_cuda_error().decode() if code == -4 else ""
         raise GqeError(name, code, detail)
@@ -200,43 +202,48 @@ def gqa_dense_forward(dims, x, Wq, Wk, Wv, Wo_dense, y, ws, stream=None) -> None
 # ---- operators around the key/value cache ----------------------------------------
 # Their tensors are checked here, before the call: each is contiguous, on the
 # current device, of the stated type and of as many elements as the dimensions
-# say. A tensor that is not raises GqeError (GQE_ERR_INVALID_ARG) and names it.
+# say (None goes on to the C entry point, which knows where it may be). A tensor
+# that is not raises GqeError (GQE_ERR_INVALID_ARG) and names it.
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _checked(fn: str, device: int, specs) -> list:
-    """Data pointers of (name, tensor, dtype, elements, needed) in order; None
-    stays None where it is not needed."""
+def _checked(fn: str, names: tuple, dtypes: tuple, tensors: tuple, sizes: tuple) -> list:
+    """Data pointers of the tensors, and the handle of the current stream."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
     out = []
-    for name, t, dtype, n, needed in specs:
+    for i, t in enumerate(tensors):
         if t is None:
-            if needed:
-                raise GqeError(fn, -1, f"{name} is missing")
             out.append(None)
             continue
-        if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
-            raise GqeError(fn, -1, f"{name} must be a contiguous {dtype} tensor of {n} elements on cuda:{device}, got "
-                                   f"{tuple(t.shape)} {t.dtype} on {t.device}"
+        if t.dtype is not dtypes[i] or t.numel() != sizes[i] or t.get_device() != device or device < 0 or not t.is_contiguous():
+            raise GqeError(fn, -1, f"{names[i]} must be a contiguous {dtypes[i]} tensor of {sizes[i]} elements on the current "
+                                   f"device (cuda:{device}), got {tuple(t.shape)} {t.dtype} on {t.device}"
                                    f"{'' if t.is_contiguous() else ', not contiguous'}")
         out.append(t.data_ptr())
     return out
+
+
+def _current(stream):
+    """_stream without the Python object of the current stream."""
+    if stream is None and torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return 0 if stream is None else _stream(stream)
 
 
 def _bytes(ws) -> int:
     return 0 if ws is None else ws.numel()
 
 
-def _run(fn: str, device: int, stream, *args) -> None:
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)  # current_stream() without its Python object
-    _call(fn, *args, _stream(stream))
-
-
-def _device(fn: str) -> int:
-    if not torch.cuda.is_available():
-        raise GqeError(fn, -6)
-    return torch.cuda.current_device()
+_ROPE_NAMES = ("Q", "K", "wq", "wk", "sel", "inv_freq", "positions", "Qo", "Ko")
+_ROPE_TYPES = (_BF, _BF, _BF, _BF, _I32, _F32, _I32, _BF, _BF)
+_TREE_NAMES = ("Q", "K_new", "V_new", "K_cache", "V_cache", "cache_len", "draft_len", "parent", "O", "lse", "ws")
+_TREE_TYPES = (_BF, _BF, _BF, _BF, _BF, _I32, _I32, _I32, _BF, _F32, _U8)
+_COMMIT_NAMES = ("path", "n_acc", "positions", "Q", "lse", "K_new", "V_new", "cache_len", "K_cache", "V_cache", "pos",
+                 "mass_in", "mass_out", "new_len")
+_COMMIT_TYPES = (_I32, _I32, _I32, _BF, _F32, _BF, _BF, _I32, _BF, _BF, _I32, _F32, _F32, _I32)
+_EVICT_NAMES = ("cache_len", "next_pos", "K_cache", "V_cache", "mass_in", "mass_out", "pos_in", "pos_out", "new_len", "ws")
+_EVICT_TYPES = (_I32, _I32, _BF, _BF, _F32, _F32, _I32, _I32, _I32, _U8)
 
 
 def gqe_qk_rope(dims, Q, K, wq, wk, sel, inv_freq, positions, Qo, Ko, *, layout=ROPE_HALF, rot=64, eps=1e-6, scale=1.0,
@@ -248,15 +255,12 @@ def gqe_qk_rope(dims, Q, K, wq, wk, sel, inv_freq, positions, Qo, Ko, *, layout=
     rope_frequencies; positions [B*T], or None for 0..T-1 in each sequence.
     Either of Q and K may be None together with its output."""
     d = dims_struct(dims)
-    fn, dev = "gqe_qk_rope", _device("gqe_qk_rope")
-    N, q, k = d.B * d.T, d.B * d.T * (d.G * d.k + 1) * 64, d.B * d.T * d.G * 64
-    need_q, need_k = Q is not None or Qo is not None, K is not None or Ko is not None
-    p = _checked(fn, dev, (("Q", Q, _BF16, q, need_q), ("K", K, _BF16, k, need_k), ("wq", wq, _BF16, (d.G * d.M + 1) * 64, False),
-                           ("wk", wk, _BF16, d.G * 64, False),
-                           ("sel", sel, _I32, N * d.G * d.k, wq is not None and Q is not None),
-                           ("inv_freq", inv_freq if rot else None, _F32, rot // 2, rot != 0), ("positions", positions, _I32, N, False),
-                           ("Qo", Qo, _BF16, q, need_q), ("Ko", Ko, _BF16, k, need_k)))
-    _run(fn, dev, stream, ctypes.byref(d), layout, rot, eps, scale, *p)
+    G, k, N = d.G, d.k, d.B * d.T
+    nq, nk = N * (G * k + 1) * 64, N * G * 64
+    p = _checked("gqe_qk_rope", _ROPE_NAMES, _ROPE_TYPES,
+                 (Q, K, wq, wk, sel, inv_freq if rot else None, positions, Qo, Ko),
+                 (nq, nk, (G * d.M + 1) * 64, G * 64, N * G * k, rot // 2, N, nq, nk))
+    _call("gqe_qk_rope", ctypes.byref(d), layout, rot, eps, scale, *p, _current(stream))
 
 
 def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0,
@@ -308,15 +312,12 @@ def gqe_tree_attn(dims, cap, Q, K_new, V_new, K_cache, V_cache, cache_len, draft
     parent [B*T] (None: a chain). draft_len [B] (None: T each). Writes O
     [B*T, G*k+1, 64] and lse [B*T, G*k+1] (or None)."""
     d = dims_struct(dims)
-    fn, dev = "gqe_tree_attn", _device("gqe_tree_attn")
-    N, Ha = d.B * d.T, d.G * d.k + 1
-    kn, kc = N * d.G * 64, d.B * cap * d.G * 64
-    p = _checked(fn, dev, (("Q", Q, _BF16, N * Ha * 64, True), ("K_new", K_new, _BF16, kn, True), ("V_new", V_new, _BF16, kn, True),
-                           ("K_cache", K_cache, _BF16, kc, True), ("V_cache", V_cache, _BF16, kc, True),
-                           ("cache_len", cache_len, _I32, d.B, True), ("draft_len", draft_len, _I32, d.B, False),
-                           ("parent", parent, _I32, N, False), ("O", O, _BF16, N * Ha * 64, True),
-                           ("lse", lse, _F32, N * Ha, False), ("ws", ws, torch.uint8, _bytes(ws), True)))
-    _run(fn, dev, stream, ctypes.byref(d), cap, *p, _bytes(ws))
+    B, G, N = d.B, d.G, d.B * d.T
+    rows, kn, kc = N * (G * d.k + 1), N * G * 64, B * cap * G * 64
+    p = _checked("gqe_tree_attn", _TREE_NAMES, _TREE_TYPES,
+                 (Q, K_new, V_new, K_cache, V_cache, cache_len, draft_len, parent, O, lse, ws),
+                 (rows * 64, kn, kn, kc, kc, B, B, N, rows * 64, rows, _bytes(ws)))
+    _call("gqe_tree_attn", ctypes.byref(d), cap, *p, _bytes(ws), _current(stream))
 
 
 def gqe_tree_commit(dims, cap, path, n_acc, positions, Q, lse, K_new, V_new, cache_len, K_cache, V_cache, pos, mass_in,
@@ -326,17 +327,12 @@ def gqe_tree_commit(dims, cap, path, n_acc, positions, Q, lse, K_new, V_new, cac
     not accumulated), pos [B, G, cap] (or None). mass_out may be mass_in;
     new_len may not be cache_len."""
     d = dims_struct(dims)
-    fn, dev = "gqe_tree_commit", _device("gqe_tree_commit")
-    N, Ha = d.B * d.T, d.G * d.k + 1
-    kn, kc, rows = N * d.G * 64, d.B * cap * d.G * 64, d.B * d.G * cap
-    m = mass_in is not None or mass_out is not None
-    p = _checked(fn, dev, (("path", path, _I32, N, False), ("n_acc", n_acc, _I32, d.B, False), ("positions", positions, _I32, N, False),
-                           ("Q", Q, _BF16, N * Ha * 64, m), ("lse", lse, _F32, N * Ha, m), ("K_new", K_new, _BF16, kn, True),
-                           ("V_new", V_new, _BF16, kn, True), ("cache_len", cache_len, _I32, d.B, True),
-                           ("K_cache", K_cache, _BF16, kc, True), ("V_cache", V_cache, _BF16, kc, True),
-                           ("pos", pos, _I32, rows, False), ("mass_in", mass_in, _F32, rows, m), ("mass_out", mass_out, _F32, rows, m),
-                           ("new_len", new_len, _I32, d.B, True)))
-    _run(fn, dev, stream, ctypes.byref(d), cap, *p)
+    B, G, N = d.B, d.G, d.B * d.T
+    rows, kn, kc, m = N * (G * d.k + 1), N * G * 64, B * cap * G * 64, B * G * cap
+    p = _checked("gqe_tree_commit", _COMMIT_NAMES, _COMMIT_TYPES,
+                 (path, n_acc, positions, Q, lse, K_new, V_new, cache_len, K_cache, V_cache, pos, mass_in, mass_out, new_len),
+                 (N, B, N, rows * 64, rows, kn, kn, B, kc, kc, m, m, m, B))
+    _call("gqe_tree_commit", ctypes.byref(d), cap, *p, _current(stream))
 
 
 def gqe_cache_evict(dims, keep, sink, recent, cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out,
@@ -346,14 +342,11 @@ def gqe_cache_evict(dims, keep, sink, recent, cache_len, next_pos, K_cache, V_ca
     then the largest mass; the cache is closed up in place. mass_out and
     pos_out may be mass_in and pos_in; new_len may not be cache_len."""
     d = dims_struct(dims)
-    fn, dev = "gqe_cache_evict", _device("gqe_cache_evict")
-    kc, rows = d.B * d.T * d.G * 64, d.B * d.G * d.T
-    p = _checked(fn, dev, (("cache_len", cache_len, _I32, d.B, True), ("next_pos", next_pos, _I32, d.B, True),
-                           ("K_cache", K_cache, _BF16, kc, True), ("V_cache", V_cache, _BF16, kc, True),
-                           ("mass_in", mass_in, _F32, rows, True), ("mass_out", mass_out, _F32, rows, True),
-                           ("pos_in", pos_in, _I32, rows, True), ("pos_out", pos_out, _I32, rows, True),
-                           ("new_len", new_len, _I32, d.B, True), ("ws", ws, torch.uint8, _bytes(ws), True)))
-    _run(fn, dev, stream, ctypes.byref(d), keep, sink, recent, *p, _bytes(ws))
+    B, m = d.B, d.B * d.G * d.T
+    p = _checked("gqe_cache_evict", _EVICT_NAMES, _EVICT_TYPES,
+                 (cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out, new_len, ws),
+                 (B, B, m * 64, m * 64, m, m, m, m, B, _bytes(ws)))
+    _call("gqe_cache_evict", ctypes.byref(d), keep, sink, recent, *p, _bytes(ws), _current(stream))
 
 
 def gqe_check_error(stream=None) -> int:

@@ -718,15 +718,16 @@ def test_tensors_of_another_kind_are_refused():
         gqe.gqe_tree_attn(d, cap, *a.values())
 
     call()
-    for kw in (dict(Q=v["Q"].float()), dict(Q=v["Q"].cpu()), dict(Q=v["Q"][:4]), dict(lens=v["lens"].long()), dict(Q=None), dict(ws=None),
+    for kw in (dict(Q=v["Q"].float()), dict(Q=v["Q"].cpu()), dict(Q=v["Q"][:4]), dict(lens=v["lens"].long()), dict(Q=None),
                dict(Kc=v["Kc"].transpose(1, 2)), dict(parent=v["parent"].view(2, 4).t()), dict(O=torch.empty(8, 10, 64, dtype=torch.bfloat16, device="cuda")[:, ::2]),
                dict(lse=lse.half())):
         with pytest.raises(gqe.GqeError) as e:
             call(**kw)
         assert e.value.code == -1
-    with pytest.raises(gqe.GqeError) as e:
-        call(ws=ws[:-256])
-    assert e.value.code == -3
+    for short in (ws[:-256], None):
+        with pytest.raises(gqe.GqeError) as e:
+            call(ws=short)
+        assert e.value.code == -3
     with pytest.raises(gqe.GqeError) as e:
         gqe.gqe_tree_attn(d, 0, *[v["Q"]] * 11)
     assert e.value.code == -1
