@@ -10,28 +10,34 @@
 // the bf16 input and the bf16 output is fp32: the result is rounded once.
 //
 // Angles: pos * inv_freq reaches 10^6 radians and more at far positions, where
-// an fp32 product has lost the angle (spacing 0.06). The turns pos * inv_freq /
-// 2 pi are taken in fp64, reduced to [-1/2, 1/2], and only then rounded to
-// fp32 for sincospi: one fp64 multiply, one subtraction and one rounding for
-// each (token, pair), shared by all heads of the token.
+// an fp32 product has lost the angle (spacing 0.06). inv_freq / 2 pi, in turns
+// a position, is therefore held as a 64-bit fraction of a turn (from fp64, once
+// a block): pos times that, modulo 2^64, is the angle modulo a turn, by three
+// integer multiplies, exact but for the fraction's own rounding (relative
+// 2^-53). As a signed number it is converted to fp32 once, so small angles keep
+// their relative precision, and goes to sincospi.
 //
-// Work: memory-bound, 256 bytes a head (read and written once). Four lanes hold
-// a head, 16 elements (two 16-byte chunks) each, so that a rotation's partners
-// are in one thread: with half = rot/2 a multiple of eight, lane l < half/8
-// takes chunks l and l + half/8, and the other lanes the chunks that are not
-// rotated, two by two; neighbouring pairs are in one chunk anyhow. Only other
-// values of half go through shared memory. A block takes `tpb` tokens, whose
-// cosines and sines it computes once into shared memory while its first loads
-// are in flight.
+// Work: memory-bound, 256 bytes a head (read and written once), so what has to
+// be kept small is the instructions a byte. Four lanes hold a head, 16 elements
+// (two 16-byte chunks) each, and a rotation's partners are in one thread: with
+// half = rot/2 a multiple of eight, lane l < half/8 takes chunks l and
+// l + half/8, and the other lanes the chunks that are not rotated, two by two;
+// neighbouring pairs are in one chunk anyhow. Only other values of half go
+// through shared memory. A thread keeps its head: the block is `tp` tokens wide
+// and walks over `tpb` tokens, so addresses advance by a constant and the key
+// weights stay in registers. Cosines and sines of the block's tokens are
+// computed once into shared memory while its first loads are in flight;
+// products are packed in pairs (f32x2).
 #pragma once
 
+#include "attn2.cuh"
 #include "sm100.cuh"
 
 namespace gqe {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 2;      // head rows a thread loads before it uses the first
-constexpr int kRopeMaxTpb = 16;    // tokens a block takes at most
+constexpr int kRopeThreads = 256;      // at most, for up to 64 heads a token
+constexpr int kRopeThreadsWide = 544;  // 129 heads (rounded up to whole warps) of one token
+constexpr int kRopeMaxTpb = 16;    // tokens of a chunk at most
 
 enum : int { kRopeInterleaved = 0, kRopeHalf8 = 1, kRopeHalfAny = 2 };
 
@@ -44,175 +50,186 @@ struct RopeParams {
   __nv_bfloat16 *Qo, *Ko;
   float eps, scale;
   int N, T, G, M, k, Ha, Hq, Hk;  // Hq = Ha or 0, Hk = G or 0
-  int rot, tpb;
+  int rot;
+  int tp, tpb;  // tokens side by side in a block, tokens of a chunk (a multiple of tp)
+  int span;     // tokens of a block (a multiple of tp)
   int log2k;
-  uint32_t inv_H;  // ceil(2^20 / (Hq + Hk)): row / H as a multiply, exact for rows < 2^20 / H
 };
 
-template <int kLayout>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams p) {
-  __shared__ float2 s_cs[kRopeMaxTpb][32];
-  __shared__ float s_row[kLayout == kRopeHalfAny ? kRopeThreads * 16 : 1];
+__device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// Two rotations: (a, b) -> (a c - b s, b c + a s).
+__device__ __forceinline__ void turn2(float& a0, float& a1, float& b0, float& b1, float c0, float c1, float s0, float s1) {
+  float x0, x1, y0, y1;
+  fmul2(x0, x1, b0, b1, -s0, -s1);
+  fmul2(y0, y1, a0, a1, s0, s1);
+  ffma2(a0, a1, a0, a1, c0, c1, x0, x1);
+  ffma2(b0, b1, b0, b1, c0, c1, y0, y1);
+}
+
+template <int kLayout, int kThreads>
+__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
+  __shared__ float4 s_cos[2][kRopeMaxTpb][8], s_sin[2][kRopeMaxTpb][8];
+  __shared__ unsigned long long s_turn[32];
+  __shared__ float s_row[kLayout == kRopeHalfAny ? kThreads * 16 : 1];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int l4 = tid & 3, grp = tid >> 2;  // lane of the head, head row of the pass
+  const int l4 = tid & 3, grp = tid >> 2;  // lane of the head; head of this thread
   const int H = p.Hq + p.Hk;
-  const int n0 = blockIdx.x * p.tpb;
-  const int ntok = min(p.tpb, p.N - n0);
-  const int rows = ntok * H;
   const int half = p.rot >> 1;
-  constexpr int kPass = kRopeThreads / 4;
+  const int tl = min(grp / H, p.tp - 1);  // (lanes past the last head repeat one and store nothing)
+  const int h = min(grp - tl * H, H - 1);
+  const bool mine = grp < p.tp * H;
+  const bool is_q = h < p.Hq;
   // this lane's two chunks of eight elements
-  int c0 = l4, c1 = l4 + 4;
+  int c0 = kLayout == kRopeInterleaved ? 2 * l4 : l4, cd = kLayout == kRopeInterleaved ? 1 : 4;  // c0 and c0 + cd
   bool turns_here = true;  // (half layout) the chunks are each other's partners
   if constexpr (kLayout == kRopeHalf8) {
     const int hc = half >> 3;
     turns_here = l4 < hc;
     c0 = turns_here ? l4 : 2 * l4;
-    c1 = turns_here ? l4 + hc : 2 * l4 + 1;
+    cd = turns_here ? hc : 1;
   }
-  uint4 buf[kRopeBatch][2];
-  auto load = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u) {
-      const int r = base + u * kPass + grp;
-      if (r < rows) {
-        const int t = (int)(((uint32_t)r * p.inv_H) >> 20), h = r - t * H;
-        const size_t n = (size_t)n0 + t;
-        const __nv_bfloat16* src = h < p.Hq ? p.Q + (n * p.Ha + h) * 64 : p.K + (n * p.G + (h - p.Hq)) * 64;
-        buf[u][0] = reinterpret_cast<const uint4*>(src)[c0];
-        buf[u][1] = reinterpret_cast<const uint4*>(src)[c1];
+  // the block's tokens are [n0, n1), this thread's n0 + tl, n0 + tl + tp, ...
+  const int n0 = blockIdx.x * p.span, n1 = min(p.N, n0 + p.span);
+  const size_t first = ((size_t)(n0 + tl) * (is_q ? p.Ha : p.G) + (is_q ? h : h - p.Hq)) * 8 + c0;
+  const uint32_t step = (uint32_t)p.tp * (is_q ? p.Ha : p.G) * 8;  // 16-byte chunks from one token to its next
+  const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.Q : p.K) + first;
+  uint4* dst = reinterpret_cast<uint4*>(is_q ? p.Qo : p.Ko) + first;
+  const bool normed = (is_q ? p.wq : p.wk) != nullptr;
+  const uint4* wt = reinterpret_cast<const uint4*>(is_q ? p.wq : p.wk) + c0;
+  const bool routed = is_q && h < p.G * p.k && normed;  // its weight row depends on the token
+  const int32_t* sel = p.sel + (size_t)(n0 + tl) * (p.G * p.k) + h;
+  const int expert0 = (h >> p.log2k) * p.M;
+  // this thread's next token: its element chunks and expert are loaded one
+  // token ahead
+  uint4 b0, b1;
+  int e_next = 0;
+  auto fetch = [&](int n) {
+    if (n < n1) {
+      b0 = src[0];
+      b1 = src[cd];
+      if (routed) e_next = sel[0];
+      src += step;
+      sel += p.tp * (p.G * p.k);
+    }
+  };
+  uint4 w0, w1;
+  auto load_weights = [&](int head) {
+    w0 = wt[head * 8];
+    w1 = wt[head * 8 + cd];
+  };
+  auto angles = [&](int chunk, int buf) {
+    for (int i = tid; i < p.tpb * 32; i += blockDim.x) {
+      const int t = i >> 5, f = i & 31, n = chunk + t;
+      if (f < half && n < n1) {
+        const int pos = p.positions ? p.positions[n] : n % p.T;
+        const long long turn = (long long)((unsigned long long)(long long)pos * s_turn[f]);
+        float s, c;
+        sincospif(__ll2float_rn(turn) * 0x1p-63f, &s, &c);
+        reinterpret_cast<float*>(s_cos[buf][t])[f] = c * p.scale;
+        reinterpret_cast<float*>(s_sin[buf][t])[f] = s * p.scale;
       }
     }
   };
-  load(0);
-  for (int i = tid; i < ntok * 32; i += kRopeThreads) {
-    const int t = i >> 5, f = i & 31;
-    if (f < half) {
-      const int n = n0 + t;
-      const int pos = p.positions ? p.positions[n] : n % p.T;
-      double turns = (double)pos * ((double)p.inv_freq[f] * 0.15915494309189533577);
-      turns -= rint(turns);
-      float s, c;
-      sincospif((float)(2.0 * turns), &s, &c);
-      s_cs[t][f] = make_float2(c * p.scale, s * p.scale);
-    }
+  fetch(n0 + tl);
+  if (normed && !routed) load_weights(is_q ? p.G * p.M : h - p.Hq);
+  if (tid < half) {
+    const double turns = (double)p.inv_freq[tid] * 0.15915494309189533577;
+    s_turn[tid] = (unsigned long long)((turns - floor(turns)) * 0x1p64);
   }
   __syncthreads();
-  for (int base = 0; base < rows; base += kPass * kRopeBatch) {
-    uint4 cur[kRopeBatch][2];
-#pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u) {
-      cur[u][0] = buf[u][0];
-      cur[u][1] = buf[u][1];
-    }
-    load(base + kPass * kRopeBatch);
-#pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u) {
-      const int r = base + u * kPass + grp;
-      // a warp holds eight rows; shuffles need all of its lanes
-      if (!__any_sync(0xffffffffu, r < rows)) break;
-      const bool live = r < rows;
-      const int rr = live ? r : rows - 1;
-      const int t = (int)(((uint32_t)rr * p.inv_H) >> 20), h = rr - t * H;
-      const size_t n = (size_t)n0 + t;
-      const bool is_q = h < p.Hq;
-      const __nv_bfloat16* wt = is_q ? p.wq : p.wk;
-      uint4 wv[2];
-      if (wt != nullptr) {
-        int head = h - p.Hq;
-        if (is_q) {
-          head = p.G * p.M;
-          if (h < p.G * p.k) {
-            const int e = p.sel[n * (p.G * p.k) + h];
-            if (e < 0 || e >= p.M) flag_bounds_error();
-            head = (h >> p.log2k) * p.M + min(max(e, 0), p.M - 1);
-          }
-        }
-        wv[0] = reinterpret_cast<const uint4*>(wt + (size_t)head * 64)[c0];
-        wv[1] = reinterpret_cast<const uint4*>(wt + (size_t)head * 64)[c1];
+  angles(n0, 0);
+  __syncthreads();
+  int buf = 0;
+  for (int chunk = n0; chunk < n1; chunk += p.tpb, buf ^= 1) {
+    if (chunk + p.tpb < n1) angles(chunk + p.tpb, buf ^ 1);
+    for (int t = tl; t < p.tpb; t += p.tp) {
+      const bool live = mine && chunk + t < n1;
+      const uint32_t u[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+      if (routed) {
+        if (e_next < 0 || e_next >= p.M) flag_bounds_error();
+        load_weights(expert0 + min(max(e_next, 0), p.M - 1));
       }
-      float y[2][8];
-      float ss = 0.f;
+      fetch(chunk + t + p.tp);
+      float y[16];  // chunk c0, then chunk c0 + cd
+      float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint32_t w32[4] = {cur[u][c].x, cur[u][c].y, cur[u][c].z, cur[u][c].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[c][2 * j] = bf16lo_to_f32(w32[j]);
-          y[c][2 * j + 1] = bf16hi_to_f32(w32[j]);
-          ss = fmaf(y[c][2 * j], y[c][2 * j], ss);
-          ss = fmaf(y[c][2 * j + 1], y[c][2 * j + 1], ss);
-        }
+      for (int j = 0; j < 8; ++j) {
+        y[2 * j] = bf16lo_to_f32(u[j]);
+        y[2 * j + 1] = bf16hi_to_f32(u[j]);
+        ffma2(s0, s1, y[2 * j], y[2 * j + 1], y[2 * j], y[2 * j + 1], s0, s1);
       }
+      float ss = s0 + s1;
       ss += __shfl_xor_sync(0xffffffffu, ss, 1);
       ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-      if (wt != nullptr) {
+      if (normed) {
         const float rs = rsqrtf(fmaf(ss, 1.f / 64.f, p.eps));
+        const uint32_t ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t ww[4] = {wv[c].x, wv[c].y, wv[c].z, wv[c].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y[c][2 * j] *= rs * bf16lo_to_f32(ww[j]);
-            y[c][2 * j + 1] *= rs * bf16hi_to_f32(ww[j]);
-          }
+        for (int j = 0; j < 8; ++j) {
+          float a, b;
+          fmul2(a, b, bf16lo_to_f32(ww[j]), bf16hi_to_f32(ww[j]), rs, rs);
+          fmul2(y[2 * j], y[2 * j + 1], y[2 * j], y[2 * j + 1], a, b);
         }
       }
       if constexpr (kLayout == kRopeInterleaved) {
+        // a chunk is four neighbouring pairs
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int f = 4 * (c ? c1 : c0) + j;
-            if (f < half) {
-              const float2 cs = s_cs[t][f];
-              const float a = y[c][2 * j], b = y[c][2 * j + 1];
-              y[c][2 * j] = fmaf(a, cs.x, -b * cs.y);
-              y[c][2 * j + 1] = fmaf(b, cs.x, a * cs.y);
-            }
+        for (int c = 0; c < 2; ++c) {
+          const int at = c0 + c;
+          const float4 cs = s_cos[buf][t][at], sn = s_sin[buf][t][at];
+          float* v = y + 8 * c;
+          if (4 * at + 4 <= half) {
+            turn2(v[0], v[2], v[1], v[3], cs.x, cs.y, sn.x, sn.y);
+            turn2(v[4], v[6], v[5], v[7], cs.z, cs.w, sn.z, sn.w);
+          } else if (4 * at < half) {  // rot ends inside the chunk
+            float z0 = 0.f, z1 = 0.f;
+            turn2(v[0], z0, v[1], z1, cs.x, 0.f, sn.x, 0.f);
+            if (4 * at + 1 < half) turn2(v[2], z0, v[3], z1, cs.y, 0.f, sn.y, 0.f);
+            if (4 * at + 2 < half) turn2(v[4], z0, v[5], z1, cs.z, 0.f, sn.z, 0.f);
           }
+        }
       } else if constexpr (kLayout == kRopeHalf8) {
         if (turns_here) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 cs = s_cs[t][c0 * 8 + j];
-            const float a = y[0][j], b = y[1][j];
-            y[0][j] = fmaf(a, cs.x, -b * cs.y);
-            y[1][j] = fmaf(b, cs.x, a * cs.y);
+          for (int q = 0; q < 2; ++q) {
+            const float4 cs = s_cos[buf][t][2 * c0 + q], sn = s_sin[buf][t][2 * c0 + q];
+            float *a = y + 4 * q, *b = y + 8 + 4 * q;
+            turn2(a[0], a[1], b[0], b[1], cs.x, cs.y, sn.x, sn.y);
+            turn2(a[2], a[3], b[2], b[3], cs.z, cs.w, sn.z, sn.w);
           }
         }
       } else {
         float* row = s_row + grp * 64;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) row[(c ? c1 : c0) * 8 + j] = y[c][j];
+        for (int j = 0; j < 16; ++j) row[(j < 8 ? c0 : c0 + cd) * 8 + (j & 7)] = y[j];
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int e = (c ? c1 : c0) * 8 + j;
-            if (e < half) {
-              const float2 cs = s_cs[t][e];
-              y[c][j] = fmaf(y[c][j], cs.x, -row[e + half] * cs.y);
-            } else if (e < p.rot) {
-              const float2 cs = s_cs[t][e - half];
-              y[c][j] = fmaf(y[c][j], cs.x, row[e - half] * cs.y);
-            }
+        for (int j = 0; j < 16; ++j) {
+          const int e = (j < 8 ? c0 : c0 + cd) * 8 + (j & 7);
+          if (e < p.rot) {
+            const bool lo = e < half;
+            const int f = lo ? e : e - half;
+            const float c = reinterpret_cast<const float*>(s_cos[buf][t])[f], s = reinterpret_cast<const float*>(s_sin[buf][t])[f];
+            y[j] = fmaf(y[j], c, (lo ? -row[e + half] : row[f]) * s);
           }
+        }
         __syncwarp();
       }
       if (live) {
-        __nv_bfloat16* dst = is_q ? p.Qo + (n * p.Ha + h) * 64 : p.Ko + (n * p.G + (h - p.Hq)) * 64;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          st_global_v4(dst + (c ? c1 : c0) * 8, pack_bf16x2(y[c][0], y[c][1]), pack_bf16x2(y[c][2], y[c][3]),
-                       pack_bf16x2(y[c][4], y[c][5]), pack_bf16x2(y[c][6], y[c][7]));
+        dst[0] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        dst[cd] = make_uint4(pack_bf16x2(y[8], y[9]), pack_bf16x2(y[10], y[11]), pack_bf16x2(y[12], y[13]), pack_bf16x2(y[14], y[15]));
       }
+      dst += step;
     }
+    __syncthreads();  // the next chunk's angles are there, and this one's are used up
   }
 }
 

@@ -105,18 +105,33 @@ int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale, 
   p.Hk = K ? d->G : 0;
   p.rot = rot;
   for (p.log2k = 0; (1 << p.log2k) < d->k;) ++p.log2k;
-  // about 256 head rows (four passes) a block, fewer tokens while that leaves
-  // SMs without a block
+  // a block: as many tokens side by side as 256 threads hold (one where a
+  // token's heads alone are more); it walks over chunks of up to 16 tokens,
+  // smaller ones while that leaves SMs without a block
   const int H = p.Hq + p.Hk;
-  p.inv_H = ((1u << 20) + H - 1) / H;
-  p.tpb = std::min(kRopeMaxTpb, std::max(1, 256 / H));
-  while (p.tpb > 1 && cdiv(p.N, p.tpb) < sm_count()) p.tpb /= 2;
-  const dim3 grid((unsigned)cdiv(p.N, p.tpb));
+  p.tp = std::min(kRopeMaxTpb, std::max(1, kRopeThreads / 4 / H));
+  p.tpb = kRopeMaxTpb / p.tp * p.tp;
+  while (p.tpb > p.tp && cdiv(p.N, p.tpb) < 4 * sm_count()) p.tpb -= p.tp;
+  if (p.N < p.tp) p.tp = p.tpb = p.N;
+  const int nchunk = (int)cdiv(p.N, p.tpb);
+  const dim3 block((unsigned)(cdiv(4 * H * p.tp, 32) * 32));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (layout == GQE_ROPE_INTERLEAVED || rot == 0)
-    return launch_pdl(qk_rope_kernel<kRopeInterleaved>, grid, dim3(kRopeThreads), 0, st, p);
-  if (rot % 16 == 0) return launch_pdl(qk_rope_kernel<kRopeHalf8>, grid, dim3(kRopeThreads), 0, st, p);
-  return launch_pdl(qk_rope_kernel<kRopeHalfAny>, grid, dim3(kRopeThreads), 0, st, p);
+  auto run = [&](auto kern) -> int {
+    int per_sm = 1;  // blocks an SM holds; asked for only where there are more chunks than SMs
+    if (nchunk > sm_count())
+      GQE_TRY(cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (int)block.x, 0)));
+    const int most = std::min(nchunk, std::max(1, per_sm) * sm_count());
+    p.span = (int)cdiv(cdiv(p.N, most), p.tp) * p.tp;
+    return launch_pdl(kern, dim3((unsigned)cdiv(p.N, p.span)), block, 0, st, p);
+  };
+  const int lay = layout == GQE_ROPE_INTERLEAVED || rot == 0 ? kRopeInterleaved : (rot % 16 == 0 ? kRopeHalf8 : kRopeHalfAny);
+  if (block.x > kRopeThreads)
+    return lay == kRopeInterleaved ? run(qk_rope_kernel<kRopeInterleaved, kRopeThreadsWide>)
+           : lay == kRopeHalf8     ? run(qk_rope_kernel<kRopeHalf8, kRopeThreadsWide>)
+                                   : run(qk_rope_kernel<kRopeHalfAny, kRopeThreadsWide>);
+  return lay == kRopeInterleaved ? run(qk_rope_kernel<kRopeInterleaved, kRopeThreads>)
+         : lay == kRopeHalf8     ? run(qk_rope_kernel<kRopeHalf8, kRopeThreads>)
+                                 : run(qk_rope_kernel<kRopeHalfAny, kRopeThreads>);
 }
 
 int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_new, const void* V_new,
