@@ -17,17 +17,18 @@
 // 2^-53). As a signed number it is converted to fp32 once, so small angles keep
 // their relative precision, and goes to sincospi.
 //
-// Work: memory-bound, 256 bytes a head (read and written once), so what has to
-// be kept small is the instructions a byte. Four lanes hold a head, 16 elements
-// (two 16-byte chunks) each, and a rotation's partners are in one thread: with
-// half = rot/2 a multiple of eight, lane l < half/8 takes chunks l and
-// l + half/8, and the other lanes the chunks that are not rotated, two by two;
-// neighbouring pairs are in one chunk anyhow. Only other values of half go
-// through shared memory. A thread keeps its head: the block is `tp` tokens wide
-// and walks over `tpb` tokens, so addresses advance by a constant and the key
-// weights stay in registers. Cosines and sines of the block's tokens are
-// computed once into shared memory while its first loads are in flight;
-// products are packed in pairs (f32x2).
+// Work: memory-bound, 256 bytes a head (read and written once). A block walks
+// over its tokens in chunks of `tpb`, whose rows of Q and of K are contiguous
+// and come by bulk copies into a ring of kRopeStages chunks: loads stay in
+// flight whatever the warps do, which is what the time hung on (4.0 TB/s at 60%
+// of the issue slots with loads through registers one token ahead). Four lanes
+// hold a head, 16 elements (two 16-byte chunks) each, and a rotation's partners
+// are in one thread: with half = rot/2 a multiple of eight, lane l < half/8
+// takes 16-byte chunks l and l + half/8, and the other lanes those that are not
+// rotated, two by two; neighbouring pairs are in one chunk anyhow. Only other
+// values of half go through shared memory. A thread keeps its head, so that
+// addresses advance by a constant; cosines and sines are computed once a chunk,
+// for the next one; products are packed in pairs (f32x2).
 #pragma once
 
 #include "attn2.cuh"
@@ -38,6 +39,7 @@ namespace gqe {
 constexpr int kRopeThreads = 256;      // at most, for up to 64 heads a token
 constexpr int kRopeThreadsWide = 544;  // 129 heads (rounded up to whole warps) of one token
 constexpr int kRopeMaxTpb = 16;    // tokens of a chunk at most
+constexpr int kRopeStages = 3;
 
 enum : int { kRopeInterleaved = 0, kRopeHalf8 = 1, kRopeHalfAny = 2 };
 
@@ -73,9 +75,13 @@ __device__ __forceinline__ void turn2(float& a0, float& a1, float& b0, float& b1
 }
 
 template <int kLayout, int kThreads>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads)
+    qk_rope_kernel(const RopeParams p) {
   __shared__ float4 s_cos[2][kRopeMaxTpb][8], s_sin[2][kRopeMaxTpb][8];
+  extern __shared__ uint8_t rope_raw[];
   __shared__ unsigned long long s_turn[32];
+  __shared__ uint64_t s_full[kRopeStages];
+  __shared__ int s_abort;
   __shared__ float s_row[kLayout == kRopeHalfAny ? kThreads * 16 : 1];
   pdl_wait();
   pdl_trigger();
@@ -98,25 +104,32 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
   }
   // the block's tokens are [n0, n1), this thread's n0 + tl, n0 + tl + tp, ...
   const int n0 = blockIdx.x * p.span, n1 = min(p.N, n0 + p.span);
-  const size_t first = ((size_t)(n0 + tl) * (is_q ? p.Ha : p.G) + (is_q ? h : h - p.Hq)) * 8 + c0;
-  const uint32_t step = (uint32_t)p.tp * (is_q ? p.Ha : p.G) * 8;  // 16-byte chunks from one token to its next
-  const uint4* src = reinterpret_cast<const uint4*>(is_q ? p.Q : p.K) + first;
-  uint4* dst = reinterpret_cast<uint4*>(is_q ? p.Qo : p.Ko) + first;
+  const int own = is_q ? p.Hq : p.Hk;  // rows a token on this thread's side
+  const uint32_t step = (uint32_t)p.tp * own * 8;  // 16-byte chunks from one token to its next
+  uint4* dst = reinterpret_cast<uint4*>(is_q ? p.Qo : p.Ko) +
+               ((size_t)(n0 + tl) * own + (is_q ? h : h - p.Hq)) * 8 + c0;
+  // its first row in a stage: the chunk's rows of Q, then those of K
+  const uint32_t at0 = (tl * own + (is_q ? h : p.tpb * p.Hq + h - p.Hq)) * 8 + c0;
+  uint8_t* ring = rope_raw + ((128u - (smem_u32(rope_raw) & 127u)) & 127u);
+  const uint32_t stage_bytes = p.tpb * H * 128;
+  auto copy = [&](int chunk, int s) {  // (one thread) a chunk's rows into stage s
+    if (chunk >= n1) return;
+    const uint32_t nt = min(p.tpb, n1 - chunk);
+    uint8_t* to = ring + s * stage_bytes;
+    mbar_arrive_expect_tx(&s_full[s], nt * H * 128);
+    if (p.Hq) bulk_load(to, p.Q + (size_t)chunk * p.Hq * 64, nt * p.Hq * 128, &s_full[s]);
+    if (p.Hk) bulk_load(to + p.tpb * p.Hq * 128, p.K + (size_t)chunk * p.Hk * 64, nt * p.Hk * 128, &s_full[s]);
+  };
   const bool normed = (is_q ? p.wq : p.wk) != nullptr;
   const uint4* wt = reinterpret_cast<const uint4*>(is_q ? p.wq : p.wk) + c0;
   const bool routed = is_q && h < p.G * p.k && normed;  // its weight row depends on the token
   const int32_t* sel = p.sel + (size_t)(n0 + tl) * (p.G * p.k) + h;
   const int expert0 = (h >> p.log2k) * p.M;
-  // this thread's next token: its element chunks and expert are loaded one
-  // token ahead
-  uint4 b0, b1;
+  // the expert of this thread's next token is loaded one token ahead
   int e_next = 0;
   auto fetch = [&](int n) {
-    if (n < n1) {
-      b0 = src[0];
-      b1 = src[cd];
-      if (routed) e_next = sel[0];
-      src += step;
+    if (routed && n < n1) {
+      e_next = sel[0];
       sel += p.tp * (p.G * p.k);
     }
   };
@@ -138,6 +151,12 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
       }
     }
   };
+  if (tid == 0) {
+    for (int s = 0; s < kRopeStages; ++s) mbar_init(&s_full[s], 1);
+    s_abort = 0;
+    fence_mbar_init();
+    for (int s = 0; s < kRopeStages; ++s) copy(n0 + s * p.tpb, s);
+  }
   fetch(n0 + tl);
   if (normed && !routed) load_weights(is_q ? p.G * p.M : h - p.Hq);
   if (tid < half) {
@@ -147,11 +166,16 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
   __syncthreads();
   angles(n0, 0);
   __syncthreads();
-  int buf = 0;
+  int buf = 0, stage = 0;
+  uint32_t parity = 0;
+  bool ok = true;
   for (int chunk = n0; chunk < n1; chunk += p.tpb, buf ^= 1) {
     if (chunk + p.tpb < n1) angles(chunk + p.tpb, buf ^ 1);
-    for (int t = tl; t < p.tpb; t += p.tp) {
+    ok = mbar_wait(&s_full[stage], parity, &s_abort);
+    const uint4* src = reinterpret_cast<const uint4*>(ring + stage * stage_bytes) + at0;
+    for (int t = tl; t < p.tpb; t += p.tp, src += step) {
       const bool live = mine && chunk + t < n1;
+      const uint4 b0 = src[0], b1 = src[cd];  // (past the last token: what the stage held)
       const uint32_t u[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
       if (routed) {
         if (e_next < 0 || e_next >= p.M) flag_bounds_error();
@@ -229,7 +253,15 @@ __global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
       }
       dst += step;
     }
-    __syncthreads();  // the next chunk's angles are there, and this one's are used up
+    // the next chunk's angles are there; this one's and its stage are used up
+    if (!(ok = __syncthreads_and(ok))) break;
+    if (tid == 0) copy(chunk + kRopeStages * p.tpb, stage);
+    if (++stage == kRopeStages) stage = 0, parity ^= 1;
+  }
+  if (!ok) {
+    // a wait ran out: let the copies in flight land before the block exits
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000ull) {}
   }
 }
 

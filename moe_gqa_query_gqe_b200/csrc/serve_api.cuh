@@ -6,9 +6,14 @@
 #include "cache.cuh"
 #include "rope.cuh"
 #include "tree.cuh"
+#include "tree_umma.cuh"
 
 namespace {
 
+#ifndef GQE_TU
+#define GQE_TU 0
+#endif
+constexpr int kTreeUmmaRows = GQE_TU;
 int check_opt(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p != nullptr && !aligned16(p)) return GQE_ERR_INVALID_ARG;
@@ -42,6 +47,39 @@ size_t tree_ws_bytes(const gqe_dims* d, float** ml, float** o, uint8_t* ws) {
   if (o) *o = b;
   return c.off;
 }
+
+// Units and workspace of the tensor-core kernel (tree_umma.cuh).
+constexpr int kTuGridMax = 148;  // one block per SM of a B200
+struct TreeUmmaPlan {
+  int u0, u1, prow;
+  long long units;
+};
+TreeUmmaPlan tree_umma_plan(const gqe_dims* d) {
+  TreeUmmaPlan t;
+  t.u0 = (int)cdiv((long long)d->T * (d->k + 1), kTuRows);
+  t.u1 = (int)cdiv((long long)d->T * d->k, kTuRows);
+  t.prow = std::min(kTuRows, d->T * (d->k + 1));
+  t.units = (long long)d->B * (t.u0 + (d->G - 1) * t.u1);
+  return t;
+}
+size_t tree_umma_ws_bytes(const gqe_dims* d, TreeUmmaParams* P, uint8_t* ws) {
+  const TreeUmmaPlan t = tree_umma_plan(d);
+  Carver c{ws};
+  const size_t rows = (size_t)2 * kTuGridMax * t.prow;
+  float* ml = c.take<float>(rows * 2);
+  float* o = c.take<float>(rows * 64);
+  int2* cta = c.take<int2>((size_t)t.units);
+  if (P) {
+    P->p.part_ml = ml;
+    P->p.part_o = o;
+    P->unit_cta = cta;
+    P->u0 = t.u0;
+    P->u1 = t.u1;
+    P->prow = t.prow;
+  }
+  return c.off;
+}
+bool tree_takes_umma(const gqe_dims* d) { return d->T * d->k > kTreeUmmaRows; }
 
 // Sequences, drafted tokens and capacity of the cache operators.
 int check_tree_dims(const gqe_dims* d, int cap) {
@@ -106,23 +144,25 @@ int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale, 
   p.rot = rot;
   for (p.log2k = 0; (1 << p.log2k) < d->k;) ++p.log2k;
   // a block: as many tokens side by side as 256 threads hold (one where a
-  // token's heads alone are more); it walks over chunks of up to 16 tokens,
-  // smaller ones while that leaves SMs without a block
+  // token's heads alone are more); it walks over chunks of about 16 KB, smaller
+  // ones while that leaves SMs without a block
   const int H = p.Hq + p.Hk;
   p.tp = std::min(kRopeMaxTpb, std::max(1, kRopeThreads / 4 / H));
-  p.tpb = kRopeMaxTpb / p.tp * p.tp;
+  p.tpb = std::max(1, std::min(kRopeMaxTpb, 128 / H) / p.tp) * p.tp;
   while (p.tpb > p.tp && cdiv(p.N, p.tpb) < 4 * sm_count()) p.tpb -= p.tp;
   if (p.N < p.tp) p.tp = p.tpb = p.N;
   const int nchunk = (int)cdiv(p.N, p.tpb);
+  const int smem = kRopeStages * p.tpb * H * 128 + 128;
   const dim3 block((unsigned)(cdiv(4 * H * p.tp, 32) * 32));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto run = [&](auto kern) -> int {
+    GQE_TRY(set_smem(kern, smem));
     int per_sm = 1;  // blocks an SM holds; asked for only where there are more chunks than SMs
     if (nchunk > sm_count())
-      GQE_TRY(cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (int)block.x, 0)));
+      GQE_TRY(cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, (int)block.x, smem)));
     const int most = std::min(nchunk, std::max(1, per_sm) * sm_count());
     p.span = (int)cdiv(cdiv(p.N, most), p.tp) * p.tp;
-    return launch_pdl(kern, dim3((unsigned)cdiv(p.N, p.span)), block, 0, st, p);
+    return launch_pdl(kern, dim3((unsigned)cdiv(p.N, p.span)), block, smem, st, p);
   };
   const int lay = layout == GQE_ROPE_INTERLEAVED || rot == 0 ? kRopeInterleaved : (rot % 16 == 0 ? kRopeHalf8 : kRopeHalfAny);
   if (block.x > kRopeThreads)
@@ -163,11 +203,30 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   p.k = d->k;
   p.Ha = d->G * d->k + 1;
   p.cap = cap;
+  p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
+  if (tree_takes_umma(d)) {
+    TreeUmmaParams P;
+    memset(&P, 0, sizeof(P));
+    P.p = p;
+    tree_umma_ws_bytes(d, &P, static_cast<uint8_t*>(ws));
+    GQE_TRY(tmap_heads(&P.tmK, K_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
+    GQE_TRY(tmap_heads(&P.tmV, V_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
+    GQE_TRY(tmap_heads(&P.tmKn, K_new, (long long)d->B * d->T, d->G, 1, kTuBlock));
+    GQE_TRY(tmap_heads(&P.tmVn, V_new, (long long)d->B * d->T, d->G, 1, kTuBlock));
+    GQE_TRY(set_smem(tree_attn_umma_kernel, TuSmem::kBytes));
+    const int ctas = std::min(sm_count(), kTuGridMax);
+    GQE_TRY(launch_pdl(tree_attn_umma_kernel, dim3((unsigned)ctas), dim3(kTuThreads), TuSmem::kBytes, st, P));
+    // a warp a row, or a block of four where the units are few and so cut into
+    // many parts
+    const long long rows = (long long)d->B * d->T * p.Ha, units = tree_umma_plan(d).units;
+    if (units * 4 >= ctas)
+      return launch_pdl(tree_umma_merge_kernel<2>, dim3((unsigned)cdiv(rows, 4)), dim3(kTuMergeThreads), 0, st, P);
+    return launch_pdl(tree_umma_merge_kernel<8>, dim3((unsigned)rows), dim3(kTuMergeThreads), 0, st, P);
+  }
   p.ntile0 = t.ntile0;
   p.nrt = t.nrt;
   // no more splits than blocks of keys
   p.nsplit = (int)std::min<long long>(t.nsplit, cdiv(cap, kTmKeys) + cdiv(d->T, kTmKeys));
-  p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
   const dim3 grid((unsigned)(t.units * p.nsplit));
   auto run = [&](auto kern) -> int {
     GQE_TRY(set_smem(kern, kTmSmem));

@@ -133,6 +133,15 @@ __device__ __forceinline__ void bulk_wait_read() {
 // All of this thread's bulk groups complete (writes performed).
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned)
+// from global into this CTA's shared memory; the bytes are counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Bring `bytes` of global memory (16-byte aligned, a multiple of 16 bytes)
 // into L2 without waiting for it.
 __device__ __forceinline__ void l2_prefetch_bulk(const void* p, uint32_t bytes) {
