@@ -415,7 +415,9 @@ int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale,
  * What a masked row holds never reaches a result, infinities and NaN included.
  * Arithmetic: S, l and O accumulate in fp32, P rounded to bf16 before P V.
  * ws : gqe_workspace_bytes(d, GQE_OP_TREE_ATTN); it does not grow with cap.
- * The result does not change from call to call (no atomics). B*cap < 2^31.
+ * No atomics: the same call gives the same bits. The keys are cut into ranges by
+ * all sequences' lengths, so a sequence's rounding can depend on its batch.
+ * B*cap < 2^31.
  */
 int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q,
                   const void* K_new, const void* V_new, const void* K_cache,

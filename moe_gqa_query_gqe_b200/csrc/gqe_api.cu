@@ -785,9 +785,7 @@ size_t gqe_workspace_bytes(const gqe_dims* d, int op) {
       c.take<__nv_bfloat16>(N * (size_t)variant_max_cols(d));              // variant A
       return c.off;
     }
-    case GQE_OP_TREE_ATTN: 
-      if (d->T > kTreeMax) return 0;
-      return tree_takes_umma(d) ? tree_umma_ws_bytes(d, nullptr, nullptr) : tree_ws_bytes(d, nullptr, nullptr, nullptr);
+    case GQE_OP_TREE_ATTN: return d->T > kTreeMax ? 0 : tree_ws_bytes(d, nullptr, nullptr);
     case GQE_OP_CACHE_EVICT: return evict_ws_bytes(d, nullptr, nullptr);
     default: return 0;
   }

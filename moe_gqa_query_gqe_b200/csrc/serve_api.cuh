@@ -20,66 +20,60 @@ int check_opt(std::initializer_list<const void*> ps) {
   return GQE_OK;
 }
 
-// Row tiles and key splits of the tree attention. The split does not depend on
-// the cache's capacity (nor does the workspace): enough blocks to fill the GPU.
+// The tree attention's kernel, its units and its grid. The tensor-core kernel
+// (tree_umma.cuh) takes more than kTreeUmmaRows rows a group, the other one
+// (tree.cuh) fewer. Neither the grid nor the workspace depends on the cache's
+// capacity.
 struct TreePlan {
-  int wr, rows, ntile0, nrt, units, nsplit;
-};
-constexpr int kTreeBlocks = 148 * 4;
-TreePlan tree_plan(const gqe_dims* d) {
-  TreePlan t;
-  const int R = d->T * d->k;
-  t.wr = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
-  t.rows = 16 * t.wr;
-  t.ntile0 = (int)cdiv(R + d->T, t.rows);
-  t.nrt = (int)cdiv(R, t.rows);
-  t.units = d->B * (t.ntile0 + (d->G - 1) * t.nrt);
-  t.nsplit = (int)std::max<long long>(1, cdiv(kTreeBlocks, t.units));
-  return t;
-}
-size_t tree_ws_bytes(const gqe_dims* d, float** ml, float** o, uint8_t* ws) {
-  const TreePlan t = tree_plan(d);
-  Carver c{ws};
-  const size_t parts = t.nsplit > 1 ? (size_t)t.units * t.nsplit * t.rows : 0;
-  float* a = c.take<float>(parts * 2);
-  float* b = c.take<float>(parts * 64);
-  if (ml) *ml = a;
-  if (o) *o = b;
-  return c.off;
-}
-
-// Units and workspace of the tensor-core kernel (tree_umma.cuh).
-constexpr int kTuGridMax = 148;  // one block per SM of a B200
-struct TreeUmmaPlan {
-  int u0, u1, prow;
+  bool umma;
+  int wr;          // row tiles of 16 a unit (tree.cuh)
+  int urows, u0, u1, prow;
+  int blocks, step;
   long long units;
 };
-TreeUmmaPlan tree_umma_plan(const gqe_dims* d) {
-  TreeUmmaPlan t;
-  t.u0 = (int)cdiv((long long)d->T * (d->k + 1), kTuRows);
-  t.u1 = (int)cdiv((long long)d->T * d->k, kTuRows);
-  t.prow = std::min(kTuRows, d->T * (d->k + 1));
-  t.units = (long long)d->B * (t.u0 + (d->G - 1) * t.u1);
+constexpr int kTreeSms = 148;  // of a B200
+TreePlan tree_plan(const gqe_dims* d) {
+  TreePlan t;
+  const int R = d->T * d->k, R0 = R + d->T;
+  t.umma = R > kTreeUmmaRows;
+  t.wr = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
+  t.urows = t.umma ? kTuRows : 16 * t.wr;
+  t.u0 = (int)cdiv(R0, t.urows);
+  t.u1 = (int)cdiv(R, t.urows);
+  t.prow = std::min(t.urows, R0);
+  const int per_seq = t.u0 + (d->G - 1) * t.u1;
+  t.units = (long long)d->B * per_seq;
+  if (t.umma) {
+    // the groups side by side where every group is one tile; else ranges over
+    // all units, whose weights differ
+    t.step = R0 <= 128 ? d->G : 1;
+    t.blocks = kTreeSms / t.step * t.step;
+  } else {
+    // as many ranges as four blocks an SM allow, one wave
+    t.step = per_seq;
+    t.blocks = std::max(1, kTreeSms * 4 / per_seq) * per_seq;
+  }
   return t;
 }
-size_t tree_umma_ws_bytes(const gqe_dims* d, TreeUmmaParams* P, uint8_t* ws) {
-  const TreeUmmaPlan t = tree_umma_plan(d);
+size_t tree_ws_bytes(const gqe_dims* d, TreeParams* p, uint8_t* ws) {
+  const TreePlan t = tree_plan(d);
   Carver c{ws};
-  const size_t rows = (size_t)2 * kTuGridMax * t.prow;
+  const size_t rows = (size_t)2 * t.blocks * t.prow;
   float* ml = c.take<float>(rows * 2);
   float* o = c.take<float>(rows * 64);
   int2* cta = c.take<int2>((size_t)t.units);
-  if (P) {
-    P->p.part_ml = ml;
-    P->p.part_o = o;
-    P->unit_cta = cta;
-    P->u0 = t.u0;
-    P->u1 = t.u1;
-    P->prow = t.prow;
+  if (p) {
+    p->part_ml = ml;
+    p->part_o = o;
+    p->unit_cta = cta;
+    p->urows = t.urows;
+    p->u0 = t.u0;
+    p->u1 = t.u1;
+    p->prow = t.prow;
+    p->step = t.step;
   }
   return c.off;
 }
-bool tree_takes_umma(const gqe_dims* d) { return d->T * d->k > kTreeUmmaRows; }
 
 // Sequences, drafted tokens and capacity of the cache operators.
 int check_tree_dims(const gqe_dims* d, int cap) {
@@ -184,9 +178,10 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   GQE_TRY(check_device());
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const TreePlan t = tree_plan(d);
-  TreeParams p;
-  memset(&p, 0, sizeof(p));
-  tree_ws_bytes(d, &p.part_ml, &p.part_o, static_cast<uint8_t*>(ws));
+  TreeUmmaParams P;
+  memset(&P, 0, sizeof(P));
+  TreeParams& p = P.p;
+  tree_ws_bytes(d, &p, static_cast<uint8_t*>(ws));
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.Kn = static_cast<const __nv_bfloat16*>(K_new);
   p.Vn = static_cast<const __nv_bfloat16*>(V_new);
@@ -204,39 +199,30 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   p.Ha = d->G * d->k + 1;
   p.cap = cap;
   p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
-  if (tree_takes_umma(d)) {
-    TreeUmmaParams P;
-    memset(&P, 0, sizeof(P));
-    P.p = p;
-    tree_umma_ws_bytes(d, &P, static_cast<uint8_t*>(ws));
+  const dim3 grid((unsigned)t.blocks);
+  if (t.umma) {
     GQE_TRY(tmap_heads(&P.tmK, K_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
     GQE_TRY(tmap_heads(&P.tmV, V_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
     GQE_TRY(tmap_heads(&P.tmKn, K_new, (long long)d->B * d->T, d->G, 1, kTuBlock));
     GQE_TRY(tmap_heads(&P.tmVn, V_new, (long long)d->B * d->T, d->G, 1, kTuBlock));
     GQE_TRY(set_smem(tree_attn_umma_kernel, TuSmem::kBytes));
-    const int ctas = std::min(sm_count(), kTuGridMax);
-    GQE_TRY(launch_pdl(tree_attn_umma_kernel, dim3((unsigned)ctas), dim3(kTuThreads), TuSmem::kBytes, st, P));
-    // a warp a row, or a block of four where the units are few and so cut into
-    // many parts
-    const long long rows = (long long)d->B * d->T * p.Ha, units = tree_umma_plan(d).units;
-    if (units * 4 >= ctas)
-      return launch_pdl(tree_umma_merge_kernel<2>, dim3((unsigned)cdiv(rows, 4)), dim3(kTuMergeThreads), 0, st, P);
-    return launch_pdl(tree_umma_merge_kernel<8>, dim3((unsigned)rows), dim3(kTuMergeThreads), 0, st, P);
+    GQE_TRY(launch_pdl(tree_attn_umma_kernel, grid, dim3(kTuThreads), TuSmem::kBytes, st, P));
+  } else {
+    auto run = [&](auto kern) -> int {
+      const int smem = kTmSmem + (d->B + 1) * 4;
+      GQE_TRY(set_smem(kern, smem));
+      return launch_pdl(kern, grid, dim3(kTmThreads), smem, st, p);
+    };
+    GQE_TRY(t.wr == 1   ? run(tree_attn_mma_kernel<1>)
+            : t.wr == 2 ? run(tree_attn_mma_kernel<2>)
+                        : run(tree_attn_mma_kernel<4>));
   }
-  p.ntile0 = t.ntile0;
-  p.nrt = t.nrt;
-  // no more splits than blocks of keys
-  p.nsplit = (int)std::min<long long>(t.nsplit, cdiv(cap, kTmKeys) + cdiv(d->T, kTmKeys));
-  const dim3 grid((unsigned)(t.units * p.nsplit));
-  auto run = [&](auto kern) -> int {
-    GQE_TRY(set_smem(kern, kTmSmem));
-    return launch_pdl(kern, grid, dim3(kTmThreads), kTmSmem, st, p);
-  };
-  GQE_TRY(t.wr == 1 ? run(tree_attn_mma_kernel<1>) : (t.wr == 2 ? run(tree_attn_mma_kernel<2>) : run(tree_attn_mma_kernel<4>)));
-  if (p.nsplit == 1) return GQE_OK;
+  // the rows that were cut: a block of threads each where the units are few and
+  // so cut into many parts, else a warp
   const long long rows = (long long)d->B * d->T * p.Ha;
-  return launch_pdl(tree_merge_kernel, dim3((unsigned)cdiv(rows, kTreeMergeThreads / 32)), dim3(kTreeMergeThreads), 0, st, p,
-                    t.rows);
+  if (t.units * 4 < t.blocks)
+    return launch_pdl(tree_merge_kernel<8>, dim3((unsigned)rows), dim3(kTreeMergeThreads), 0, st, p);
+  return launch_pdl(tree_merge_kernel<2>, dim3((unsigned)cdiv(rows, 4)), dim3(kTreeMergeThreads), 0, st, p);
 }
 
 int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path, const int32_t* n_acc, const int32_t* positions,

@@ -7,7 +7,7 @@
 // other, are cut into gridDim.x ranges of equal weight, one persistent block of
 // threads (one per SM) each: whatever the lengths and however few the
 // sequences, every SM streams the same share. A unit that a range's end cuts is
-// left as partial (m, l, O) rows for tree_umma_merge_kernel, at most two of
+// left as partial (m, l, O) rows for tree_merge_kernel, at most two of
 // them per range; the others are written at once.
 //
 // Inside a unit two tiles A and B run side by side, each with its MMA thread
@@ -15,8 +15,13 @@
 //   a unit of more than 128 rows   A and B hold its two row tiles, and every
 //                                  K/V block serves both;
 //   else                           A and B hold the same rows and take the
-//                                  blocks in turn, A the even, B the odd ones,
-//                                  and are added at the end.
+//                                  blocks in turn, A the even, B the odd ones.
+//                                  With 64 rows or fewer a tile holds them
+//                                  twice, with 32 or fewer four times: each
+//                                  copy takes its half or quarter of the block's
+//                                  keys (P is zero in the others), so that all
+//                                  four warps share the exponentials. Tiles and
+//                                  copies are added at the end.
 // A pair block costs half again what a block of the second kind does (weights 3
 // and 2): it is bound by exponentials, the other by the cache's bytes.
 //
@@ -45,7 +50,6 @@ namespace gqe {
 constexpr int kTuStages = 5;
 constexpr int kTuThreads = 384;
 constexpr int kTuRegsLow = 88, kTuRegsHigh = 208;  // 88*128 + 208*256 = 168*384
-constexpr int kTuMaxB = 1024;                      // B * G * M <= 8192 and G * M >= 8
 constexpr int kTuBlock = 128;                      // keys of a block
 constexpr int kTuRows = 256;                       // rows of a unit
 constexpr int kTuPolyEvery = 8;  // every n-th pair of exponentials on the FMA pipe (as in attn2.cuh)
@@ -53,21 +57,19 @@ constexpr int kTuPolyEvery = 8;  // every n-th pair of exponentials on the FMA p
 struct TreeUmmaParams {
   CUtensorMap tmK, tmV;    // caches as [B*cap][G][64], box (64, 1, 128)
   CUtensorMap tmKn, tmVn;  // drafts as [B*T][G][64]
-  TreeParams p;            // part_ml, part_o: [2 * gridDim.x][prow] rows
-  int2* unit_cta;          // [units] first and last range that holds blocks of the unit
-  int u0, u1;              // units of group 0 and of each other group, for T tokens
-  int prow;                // rows a part holds, the most that a unit has
+  TreeParams p;            // p.step = G: the groups side by side, range r of group g is block r * G + g; 1: range r is block r
 };
 
 struct TuSmem {
   static constexpr int kQ = 0;                               // Q_A, Q_B
+  static constexpr int kSum = 0;                             // [256][32] fp32: half of both tiles' O, at a unit's end
   static constexpr int kKV = 32768;                          // stages of K, V
   static constexpr int kMask = kKV + kTuStages * 32768;      // [2][128] ancestor masks
   static constexpr int kUp = kMask + 2 * kTreeMax * 16;      // [128] pointers of the doubling
   static constexpr int kBad = kUp + kTreeMax * 4;            // [2][4] drafts with values that are not finite
   static constexpr int kML = kBad + 32;                      // [2][128] m, l of the tiles
   static constexpr int kPrefix = kML + 2 * 128 * 8;          // [B + 1] weight before each sequence
-  static constexpr int kBar = kPrefix + (kTuMaxB + 1) * 8;
+  static constexpr int kBar = kPrefix + (kTreeMaxB + 1) * 8;
   static constexpr int kBytes = kBar + 512 + 1024;
 };
 
@@ -82,7 +84,7 @@ struct TuItem {
     if (pair) return j1 - j0;
     return (j1 - j0 + 1 - t) >> 1;
   }
-  __device__ __forceinline__ bool owns(int t, int jj) const { return pair || (jj & 1) == t; }
+  __device__ __forceinline__ int copies() const { return rows > 64 ? 1 : (rows > 32 ? 2 : 4); }
   __device__ __forceinline__ int row_base(int t) const { return s * kTuRows + (pair ? t * 128 : 0); }
   __device__ __forceinline__ bool has_drafts() const { return j1 == nblk; }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nblk; }
@@ -95,32 +97,28 @@ __device__ __forceinline__ long long tu_group_weight(int R) {
   const int full = R / kTuRows, rest = R % kTuRows;
   return (long long)full * 3 + (rest ? tu_weight(rest) : 0);
 }
-__device__ __forceinline__ long long tu_seq_weight(int L, int n, int G, int k) {
-  if (n == 0) return 0;
+__device__ __forceinline__ long long tu_seq_weight(int L, int n, int G, int k, bool aligned) {
   const long long nblk = (L + kTuBlock - 1) / kTuBlock + 1;
+  if (aligned) return nblk * 2;
   return nblk * (tu_group_weight(n * (k + 1)) + (long long)(G - 1) * tu_group_weight(n * k));
 }
-__device__ __forceinline__ long long tu_range(long long total, int c, int grid) { return total * c / grid; }
-__device__ __forceinline__ int tu_range_of(long long total, int grid, long long x) {
-  return (int)(((x + 1) * grid - 1) / total);
-}
-
 // The units that a range of weight [x0, x1) holds blocks of, in order. A block
 // belongs to the range that its first weight falls into.
 struct TuCursor {
   long long x0, x1, base;
   int b, g, s;
-  __device__ __forceinline__ void start(const TreeParams& p, const long long* prefix, long long a, long long e) {
+  int only;  // the group that this block takes, or -1: all
+  __device__ __forceinline__ void start(const TreeParams& p, const long long* prefix, long long a, long long e, int group) {
     x0 = a;
     x1 = e;
-    int lo = 0, hi = p.B - 1;  // the last sequence that begins at or before x0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= x0) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
+    b = tree_first(prefix, p.B, x0);
     g = s = 0;
-    base = prefix[lo];
+    base = prefix[b];
+    only = group;
+    if (group >= 0) {
+      g = group;
+      return;
+    }
     int L, n;
     tree_lens(p.cache_len, p.draft_len, b, p.cap, p.T, L, n);
     if (n > 0 && p.G > 1) {  // straight to the group
@@ -141,7 +139,9 @@ struct TuCursor {
       it.rows = min(it.R - s * kTuRows, kTuRows);
       if (it.rows <= 0) {
         s = 0;
-        if (it.n == 0 || ++g == p.G) {
+        if (only >= 0) {
+          ++b;
+        } else if (it.n == 0 || ++g == p.G) {
           g = 0;
           ++b;
         }
@@ -152,7 +152,7 @@ struct TuCursor {
       it.s = s;
       it.pair = it.rows > 128;
       it.nblk = (it.L + kTuBlock - 1) / kTuBlock + 1;
-      it.unit = b * (P.u0 + (p.G - 1) * P.u1) + (g == 0 ? s : P.u0 + (g - 1) * P.u1 + s);
+      it.unit = b * (p.u0 + (p.G - 1) * p.u1) + (g == 0 ? s : p.u0 + (g - 1) * p.u1 + s);
       const int w = tu_weight(it.rows);
       const long long a = x0 - base, e = x1 - base;
       it.j0 = a <= 0 ? 0 : (int)min((long long)it.nblk, (a + w - 1) / w);
@@ -185,11 +185,136 @@ __device__ __forceinline__ void exp2_poly4(float& y0, float& y1, float x0, float
   y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
+constexpr int kTuPiece = 4;  // columns a thread finishes at a time
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Three-way maximum that keeps NaN.
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// The barriers and tensor-memory addresses of one tile's softmax warps.
+struct TuTile {
+  uint64_t *s_free, *pv_done, *p_full;
+  volatile int* abort_flag;
+  uint32_t tm_s, tm_o, tm_p;
+  float sl2;
+};
+
+template <int D>
+__device__ __forceinline__ void tu_load_scores(uint32_t taddr, float (&s)[128 / D]) {
+  if constexpr (D == 1) {
+    tmem_ld128f(taddr, s);
+  } else {
+    uint32_t r[128 / D];
+    if constexpr (D == 2) tmem_ld64(taddr, r); else tmem_ld32(taddr, r);
+#pragma unroll
+    for (int i = 0; i < 128 / D; ++i) s[i] = __uint_as_float(r[i]);
+  }
+}
+template <int D>
+__device__ __forceinline__ void tu_store_p(uint32_t taddr, const uint32_t (&pk)[64 / D]) {
+  if constexpr (D == 1) {
+    tmem_st64(taddr, pk);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4 / D; ++h) {
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = pk[h * 16 + i];
+      tmem_st16(taddr + h * 16, r);
+    }
+  }
+}
+
+// One block of keys for a thread's row: its 128 / D scores (columns col0 on),
+// softmax, P. `valid` keys of the block are there; with kDrafts the row sees
+// those of `mk`. First: the unit's first block of this tile.
+template <int D, bool kDrafts>
+__device__ __forceinline__ bool tu_block(const TuTile& T, int col0, int valid, const uint4& mk, bool first, uint32_t cnt,
+                                         float& m_run, float& l_run) {
+  constexpr int N = 128 / D;
+  float s[N];
+  tu_load_scores<D>(T.tm_s + col0, s);
+  tc_fence_before();
+  mbar_arrive(T.s_free);  // S may be overwritten by the next block's QK^T now
+  if constexpr (kDrafts) {
+#pragma unroll
+    for (int w = 0; w < N / 32; ++w) {
+      const uint32_t bits = D == 1 ? mask_word(mk, w) : mask_word(mk, col0 / 32 + w);
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (!((bits >> c) & 1u)) s[w * 32 + c] = -INFINITY;
+    }
+  } else if (valid < kTuBlock) {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (col0 + c >= valid) s[c] = -INFINITY;
+  }
+  float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int c = 4; c < N; c += 8) {
+    m4[0] = fmax3_nan(m4[0], s[c], s[c + 1]);
+    m4[1] = fmax3_nan(m4[1], s[c + 2], s[c + 3]);
+    if (c + 4 < N) {
+      m4[2] = fmax3_nan(m4[2], s[c + 4], s[c + 5]);
+      m4[3] = fmax3_nan(m4[3], s[c + 6], s[c + 7]);
+    }
+  }
+  const float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[1]), m4[2], m4[3]);
+  const float m_new = fmaxf(m_run, mx * T.sl2);
+  const float m_use = (m_new > m_run + kRescaleThreshold) ? m_new : m_run;
+  const float mu = m_use == -INFINITY ? 0.f : m_use;  // (nothing seen yet)
+  const float alpha = ex2_approx(m_run - mu);
+  const bool rescale = !first && m_use != m_run;
+  m_run = m_use;
+  float sm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  uint32_t pk[N / 2];
+#pragma unroll
+  for (int pi = 0; pi < N / 2; ++pi) {
+    float x0, x1, y0, y1;
+    ffma2(x0, x1, s[2 * pi], s[2 * pi + 1], T.sl2, T.sl2, -mu, -mu);
+    // (a masked place of the draft block must be exactly zero: MUFU only; with
+    // copies the exponentials bind nothing)
+    if (D == 1 && !kDrafts && (pi % kTuPolyEvery) == kTuPolyEvery - 1) {
+      exp2_poly4(y0, y1, x0, x1);
+    } else {
+      y0 = ex2_approx(x0);
+      y1 = ex2_approx(x1);
+    }
+    fadd2(sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], y0, y1);
+    pk[pi] = pack_bf16x2(y0, y1);
+  }
+  l_run = l_run * alpha + (((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7])));
+  if (!(mx < INFINITY)) l_run = __int_as_float(0x7fffffff);  // a score that is NaN or +inf: the row is NaN
+  if (!first) {
+    const bool w_ok = mbar_wait(T.pv_done, (cnt - 1) & 1, T.abort_flag);
+    if (!__all_sync(0xffffffffu, w_ok)) return false;
+    tc_fence_after();
+    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t o[16];
+        tmem_ld16(T.tm_o + h * 16, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+        tmem_st16(T.tm_o + h * 16, o);
+      }
+    }
+  }
+  tu_store_p<D>(T.tm_p + col0 / 2, pk);
+  tc_fence_before();
+  mbar_arrive(T.p_full);
+  return true;
 }
 
 __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __grid_constant__ TreeUmmaParams P) {
@@ -200,16 +325,17 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBar);
   uint64_t* k_full = bars;                  // [kTuStages]
   uint64_t* v_full = k_full + kTuStages;    // [kTuStages]
-  uint64_t* kv_empty = v_full + kTuStages;  // [kTuStages]
-  uint64_t* q_full = kv_empty + kTuStages;  // [2] tiles
+  uint64_t* k_empty = v_full + kTuStages;   // [kTuStages] two arrivals: each tile's, or two of the tile whose block it is
+  uint64_t* v_empty = k_empty + kTuStages;  // [kTuStages]
+  uint64_t* q_full = v_empty + kTuStages;   // [2] tiles
   uint64_t* s_full = q_full + 2;            // [2]
   uint64_t* s_free = s_full + 2;            // [2]
   uint64_t* p_full = s_free + 2;            // [2]
   uint64_t* pv_done = p_full + 2;           // [2]
   uint64_t* mask_full = pv_done + 2;        // [2] buffers
   uint64_t* mask_empty = mask_full + 2;     // [2]
-  uint64_t* both = mask_empty + 2;          // [2] both tiles' softmax threads meet: m, l written; O read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(both + 2);
+  uint64_t* both = mask_empty + 2;          // both tiles' softmax threads meet
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(both + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   long long* prefix = reinterpret_cast<long long*>(smem + S::kPrefix);
   uint4* s_mask = reinterpret_cast<uint4*>(smem + S::kMask);
@@ -221,7 +347,8 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
     for (int s = 0; s < kTuStages; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&kv_empty[s], 2);
+      mbar_init(&k_empty[s], 2);
+      mbar_init(&v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 128);
@@ -231,8 +358,8 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       mbar_init(&pv_done[t], 1);
       mbar_init(&mask_full[t], 32);
       mbar_init(&mask_empty[t], 256);
-      mbar_init(&both[t], 256);
     }
+    mbar_init(both, 256);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&P.tmK);
@@ -243,59 +370,72 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_wait();
   pdl_trigger();
-  // weight before each sequence (inclusive sums, shifted by one)
-  if (tid == 0) prefix[0] = 0;
-  for (int b = tid; b < p.B; b += kTuThreads) {
-    int L, n;
-    tree_lens(p.cache_len, p.draft_len, b, p.cap, p.T, L, n);
-    prefix[b + 1] = tu_seq_weight(L, n, p.G, p.k);
-  }
-  __syncthreads();
-  for (int d = 1; d < p.B; d *= 2) {
-    long long v[(kTuMaxB + kTuThreads - 1) / kTuThreads];
-#pragma unroll
-    for (int i = 0; i < (kTuMaxB + kTuThreads - 1) / kTuThreads; ++i) {
-      const int b = tid + i * kTuThreads;
-      if (b < p.B) v[i] = prefix[b + 1] + (b >= d ? prefix[b + 1 - d] : 0);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < (kTuMaxB + kTuThreads - 1) / kTuThreads; ++i) {
-      const int b = tid + i * kTuThreads;
-      if (b < p.B) prefix[b + 1] = v[i];
-    }
-    __syncthreads();
-  }
+  tree_prefix<kTuThreads>(p, prefix, [&](int L, int n) { return tu_seq_weight(L, n, p.G, p.k, p.step > 1); });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t sbase = smem_u32(smem);
-  // no range below the weight of a block, so that every range inside a unit
-  // holds one
+  // ranges: `step` blocks of threads (one a group, or one) take each; none is
+  // below the weight of a block, so that every range inside a unit holds one
   const long long total = prefix[p.B];
-  const int grid = (int)max(1ll, min((long long)gridDim.x, total / 3)), cta = blockIdx.x;
+  const int step = p.step, cta = blockIdx.x;
+  const int grid = (int)max(1ll, min((long long)(gridDim.x / step), total / 3));
+  const int range = min(cta / step, grid);
   TuCursor cur;
-  cur.start(p, prefix, tu_range(total, min(cta, grid), grid), tu_range(total, min(cta + 1, grid), grid));
-  TuItem it;
+  cur.start(p, prefix, tree_range(total, range, grid), tree_range(total, min(range + 1, grid), grid), step > 1 ? cta % step : -1);
+  TuItem it = {};
 
   if (warp < 4) {
     setmaxnreg_dec<kTuRegsLow>();
     if (warp == 0 && lane == 0) {
-      // ---- producer ----------------------------------------------------------------
-      uint32_t kv = 0;
-      bool ok = true;
-      while (ok && cur.next(P, it)) {
-        for (int j = it.j0; j < it.j1; ++j, ++kv) {
-          const int s = kv % kTuStages;
-          if (!(ok = mbar_wait(&kv_empty[s], ((kv / kTuStages) & 1) ^ 1, abort_flag))) break;
-          const bool drafts = j == it.nblk - 1;
-          const int row = drafts ? it.b * p.T : it.b * p.cap + j * kTuBlock;
-          uint8_t* to = smem + S::kKV + s * 32768;
-          mbar_arrive_expect_tx(&k_full[s], 16384);
-          tma_load_3d(to, drafts ? &P.tmKn : &P.tmK, &k_full[s], 0, it.g, row);
-          mbar_arrive_expect_tx(&v_full[s], 16384);
-          tma_load_3d(to + 16384, drafts ? &P.tmVn : &P.tmV, &v_full[s], 0, it.g, row);
+      // ---- producer: K and V each as soon as their own stage is free (K's is when
+      // its scores are done, long before V's) ----------------------------------------
+      struct Stream {
+        TuCursor cur;
+        TuItem it;
+        int j;
+        uint32_t n;
+        bool done;
+      };
+      Stream str[2] = {{cur, it, 0, 0, false}, {cur, it, 0, 0, false}};
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        str[v].done = !str[v].cur.next(P, str[v].it);
+        if (!str[v].done) str[v].j = str[v].it.j0;
+      }
+      unsigned long long idle = 0;  // since when neither could go on
+      for (uint32_t spin = 0; !(str[0].done && str[1].done); ++spin) {
+        bool moved = false;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          Stream& a = str[v];
+          const int s = a.n % kTuStages;
+          if (a.done || !mbar_test(v ? &v_empty[s] : &k_empty[s], ((a.n / kTuStages) & 1) ^ 1)) continue;
+          const bool drafts = a.j == a.it.nblk - 1;
+          const int row = drafts ? a.it.b * p.T : a.it.b * p.cap + a.j * kTuBlock;
+          uint64_t* full = v ? &v_full[s] : &k_full[s];
+          mbar_arrive_expect_tx(full, 16384);
+          tma_load_3d(smem + S::kKV + s * 32768 + v * 16384, v ? (drafts ? &P.tmVn : &P.tmV) : (drafts ? &P.tmKn : &P.tmK),
+                      full, 0, a.it.g, row);
+          ++a.n;
+          moved = true;
+          if (++a.j == a.it.j1) {
+            a.done = !a.cur.next(P, a.it);
+            if (!a.done) a.j = a.it.j0;
+          }
+        }
+        if (moved) {
+          idle = 0;
+        } else if ((spin & 63u) == 0) {
+          if (*abort_flag) break;
+          const unsigned long long now = globaltimer_ns();
+          if (idle == 0) idle = now;
+          if (now - idle > kWaitTimeoutNs) {
+            *abort_flag = 1;
+            atomicExch(&g_error_word, kDevErrTimeout);
+            break;
+          }
         }
       }
     } else if ((warp == 1 || warp == 2) && lane == 0) {
@@ -306,9 +446,11 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       uint32_t kv = 0, s_cnt = 0, pv_cnt = 0, q_cnt = 0;
       bool ok = true;
       const uint32_t qa = sbase + S::kQ + t * 16384;
-      auto issue_s = [&](uint32_t kvi) -> bool {
-        if (!mbar_wait(&k_full[kvi % kTuStages], (kvi / kTuStages) & 1, abort_flag)) return false;
-        if (s_cnt > 0 && !mbar_wait(&s_free[t], (s_cnt - 1) & 1, abort_flag)) return false;
+      auto s_ready = [&](uint32_t kvi) {
+        return mbar_test(&k_full[kvi % kTuStages], (kvi / kTuStages) & 1) &&
+               (s_cnt == 0 || mbar_test(&s_free[t], (s_cnt - 1) & 1));
+      };
+      auto issue_s = [&](uint32_t kvi, bool alone) {  // (ready)
         tc_fence_after();
         const uint32_t ka = sbase + S::kKV + (kvi % kTuStages) * 32768;
 #pragma unroll
@@ -316,36 +458,51 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
           umma_ss(tmem_base + t * 128, sdesc_sw128(qa + kk * 32, 16, 1024), sdesc_sw128(ka + kk * 32, 16, 1024), idesc_s,
                   kk != 0);
         umma_commit(&s_full[t]);
+        umma_commit(&k_empty[kvi % kTuStages]);
+        if (alone) umma_commit(&k_empty[kvi % kTuStages]);
         ++s_cnt;
-        return true;
+      };
+      auto wait_s = [&](uint32_t kvi) {
+        return mbar_wait(&k_full[kvi % kTuStages], (kvi / kTuStages) & 1, abort_flag) &&
+               (s_cnt == 0 || mbar_wait(&s_free[t], (s_cnt - 1) & 1, abort_flag));
       };
       while (ok && cur.next(P, it)) {
-        const int nj = it.j1 - it.j0, mine = it.tile_blocks(t);
+        const int nj = it.j1 - it.j0;
         const int stride = it.pair ? 1 : 2, first = it.pair ? 0 : t;
         if (!(ok = mbar_wait(&q_full[t], q_cnt & 1, abort_flag))) break;
         ++q_cnt;
-        if (mine > 0 && !(ok = issue_s(kv + first))) break;
-        for (int jj = 0; ok && jj < nj; ++jj) {
+        if (first < nj) {
+          if (!(ok = wait_s(kv + first))) break;
+          issue_s(kv + first, !it.pair);
+        }
+        for (int jj = first; jj < nj; jj += stride) {
           const uint32_t kvj = kv + jj;
-          if (it.owns(t, jj)) {
-            if (jj + stride < nj && !(ok = issue_s(kvj + stride))) break;
-            if (!(ok = mbar_wait(&v_full[kvj % kTuStages], (kvj / kTuStages) & 1, abort_flag))) break;
-            if (!(ok = mbar_wait(&p_full[t], pv_cnt & 1, abort_flag))) break;
-            tc_fence_after();
-            const uint32_t va = sbase + S::kKV + (kvj % kTuStages) * 32768 + 16384;
+          // the next block's scores as soon as its K is there, but P V does not
+          // wait for them: V's stage is what the loads behind it wait for
+          bool ahead = jj + stride < nj;
+          for (uint32_t i = 0; ahead && i < 100000000u && !mbar_test(&p_full[t], pv_cnt & 1); ++i) {
+            if (s_ready(kvj + stride)) {
+              issue_s(kvj + stride, !it.pair);
+              ahead = false;
+            } else if ((i & 1023u) == 1023u && *abort_flag) {
+              break;
+            }
+          }
+          if (!(ok = mbar_wait(&p_full[t], pv_cnt & 1, abort_flag))) break;
+          if (!(ok = mbar_wait(&v_full[kvj % kTuStages], (kvj / kTuStages) & 1, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t va = sbase + S::kKV + (kvj % kTuStages) * 32768 + 16384;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts(tmem_base + 256 + t * 64, tmem_base + 384 + t * 64 + kk * 8, sdesc_sw128(va + kk * 2048, 8192, 1024),
-                      idesc_o, (jj != first || kk != 0) ? 1u : 0u);
-            umma_commit(&pv_done[t]);
-            ++pv_cnt;
-            umma_commit(&kv_empty[kvj % kTuStages]);
-          } else {
-            // the other tile's block: released only after it has arrived (an
-            // earlier arrival would count for the stage's previous block)
-            if (!(ok = mbar_wait(&k_full[kvj % kTuStages], (kvj / kTuStages) & 1, abort_flag))) break;
-            if (!(ok = mbar_wait(&v_full[kvj % kTuStages], (kvj / kTuStages) & 1, abort_flag))) break;
-            mbar_arrive(&kv_empty[kvj % kTuStages]);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem_base + 256 + t * 64, tmem_base + 384 + t * 64 + kk * 8, sdesc_sw128(va + kk * 2048, 8192, 1024),
+                    idesc_o, (jj != first || kk != 0) ? 1u : 0u);
+          umma_commit(&pv_done[t]);
+          ++pv_cnt;
+          umma_commit(&v_empty[kvj % kTuStages]);
+          if (!it.pair) umma_commit(&v_empty[kvj % kTuStages]);
+          if (ahead) {
+            if (!(ok = wait_s(kvj + stride))) break;
+            issue_s(kvj + stride, !it.pair);
           }
         }
         kv += nj;
@@ -429,18 +586,26 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
     const int q = warp & 3;
     const int row = q * 32 + lane;  // of the tile
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    const uint32_t tm_s = tmem_base + lane_off + t * 128;
-    const uint32_t tm_o = tmem_base + lane_off + 256 + t * 64;
-    const uint32_t tm_p = tmem_base + lane_off + 384 + t * 64;
-    const float sl2 = p.scale_log2;
-    uint32_t kv = 0;             // blocks of the range before this unit's
-    uint32_t cnt = 0, other = 0; // blocks that this tile and the other have processed
+    const TuTile T = {&s_free[t], &pv_done[t], &p_full[t], abort_flag, tmem_base + lane_off + t * 128,
+                      tmem_base + lane_off + 256 + t * 64, tmem_base + lane_off + 384 + t * 64, p.scale_log2};
+    float4* sums = reinterpret_cast<float4*>(smem + S::kSum);
+    uint32_t kv = 0;   // blocks of the range before this unit's
+    uint32_t cnt = 0;  // blocks that this tile has processed
     uint32_t masks = 0, meets = 0;
     bool ok = true;
+    // all 256 softmax threads
+    auto meet = [&]() -> bool {
+      mbar_arrive(both);
+      const bool w_ok = mbar_wait(both, meets & 1, abort_flag);
+      ++meets;
+      return __all_sync(0xffffffffu, w_ok);
+    };
     while (ok && cur.next(P, it)) {
-      const int base = it.row_base(t), r = base + row;
-      const int nrow = min(128, it.R - base);          // rows of this tile
-      const bool warp_on = q * 32 < nrow;
+      const int D = it.copies(), width = 128 / D;      // rows a copy has room for
+      const int copy = row / width;
+      const int base = it.row_base(t), r = base + row % width;
+      const int nrow = min(width, it.R - base);        // rows of this tile
+      const bool warp_on = q * 32 % width < nrow;
       const int rc = min(r, it.R - 1);                 // (rows past the last repeat it and are not stored)
       const int tok = tree_row_token(rc, it.n, p.k), slot = tree_row_slot(rc, it.n, it.g, p.k, p.G);
       const size_t out = ((size_t)it.b * p.T + tok) * p.Ha + slot;
@@ -455,6 +620,12 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
 #pragma unroll
         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(qs + ((c ^ (row & 7)) << 4)) = v[c];
         fence_proxy_async_smem();
+        if (D > 1) {
+          // P of the keys that are other copies': zero for the whole unit
+          const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tmem_st16(T.tm_p + h * 16, z);
+        }
         mbar_arrive(&q_full[t]);
       }
       const int nj = it.j1 - it.j0;
@@ -497,196 +668,147 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
           mbar_arrive(&p_full[t]);
           continue;
         }
-        float s[128];
-        tmem_ld128f(tm_s, s);
-        tc_fence_before();
-        mbar_arrive(&s_free[t]);  // S may be overwritten by the next block's QK^T now
+        const int col0 = copy * width;
         if (drafts) {
           const uint4 mk = s_mask[(masks & 1) * kTreeMax + tok];
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!((mask_word(mk, c >> 5) >> (c & 31)) & 1u)) s[c] = -INFINITY;
-        } else if (valid < kTuBlock) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= valid) s[c] = -INFINITY;
-        }
-        float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < 128; c += 8) {
-          m4[0] = fmax3_nan(m4[0], s[c], s[c + 1]);
-          m4[1] = fmax3_nan(m4[1], s[c + 2], s[c + 3]);
-          if (c + 4 < 128) {
-            m4[2] = fmax3_nan(m4[2], s[c + 4], s[c + 5]);
-            m4[3] = fmax3_nan(m4[3], s[c + 6], s[c + 7]);
-          }
-        }
-        const float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[1]), m4[2], m4[3]);
-        const float m_new = fmaxf(m_run, mx * sl2);
-        const float m_use = (m_new > m_run + kRescaleThreshold) ? m_new : m_run;
-        const float mu = m_use == -INFINITY ? 0.f : m_use;
-        const float alpha = ex2_approx(m_run - mu);
-        const bool rescale = jj != first && m_use != m_run;
-        m_run = m_use;
-        float sm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[64];
-        if (drafts) {
-          // (a masked place must be exactly zero here: MUFU only)
-#pragma unroll
-          for (int pi = 0; pi < 64; ++pi) {
-            float x0, x1;
-            ffma2(x0, x1, s[2 * pi], s[2 * pi + 1], sl2, sl2, -mu, -mu);
-            const float y0 = ex2_approx(x0), y1 = ex2_approx(x1);
-            fadd2(sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], y0, y1);
-            pk[pi] = pack_bf16x2(y0, y1);
-          }
+          ok = D == 1   ? tu_block<1, true>(T, 0, valid, mk, jj == first, cnt, m_run, l_run)
+               : D == 2 ? tu_block<2, true>(T, col0, valid, mk, jj == first, cnt, m_run, l_run)
+                        : tu_block<4, true>(T, col0, valid, mk, jj == first, cnt, m_run, l_run);
         } else {
-#pragma unroll
-          for (int pi = 0; pi < 64; ++pi) {
-            float x0, x1, y0, y1;
-            ffma2(x0, x1, s[2 * pi], s[2 * pi + 1], sl2, sl2, -mu, -mu);
-            if ((pi % kTuPolyEvery) == kTuPolyEvery - 1) {
-              exp2_poly4(y0, y1, x0, x1);
-            } else {
-              y0 = ex2_approx(x0);
-              y1 = ex2_approx(x1);
-            }
-            fadd2(sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], y0, y1);
-            pk[pi] = pack_bf16x2(y0, y1);
-          }
+          const uint4 mk = make_uint4(0u, 0u, 0u, 0u);
+          ok = D == 1   ? tu_block<1, false>(T, 0, valid, mk, jj == first, cnt, m_run, l_run)
+               : D == 2 ? tu_block<2, false>(T, col0, valid, mk, jj == first, cnt, m_run, l_run)
+                        : tu_block<4, false>(T, col0, valid, mk, jj == first, cnt, m_run, l_run);
         }
-        l_run = l_run * alpha + (((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7])));
-        if (!(mx < INFINITY)) l_run = __int_as_float(0x7fffffff);  // a score that is NaN or +inf: the row is NaN
-        if (jj != first) {
-          w_ok = mbar_wait(&pv_done[t], (cnt - 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-          tc_fence_after();
-          if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              uint32_t o[16];
-              tmem_ld16(tm_o + h * 16, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st16(tm_o + h * 16, o);
-            }
-          }
-        }
-        tmem_st64(tm_p, pk);
-        tc_fence_before();
-        mbar_arrive(&p_full[t]);
+        if (!ok) break;
       }
       if (!ok) break;
-      const int nother = it.pair ? nj : (nj + t) >> 1;  // blocks of the other tile
-      other += nother;
       const int mine = it.tile_blocks(t);
       // ---- the unit's end ------------------------------------------------------------
       bool w_ok = mine == 0 || mbar_wait(&pv_done[t], (cnt - 1) & 1, abort_flag);
+      // the drafts that are not finite and their masks (waited for already by
+      // the tile whose block it was)
+      const bool fix = it.has_drafts();
+      w_ok = w_ok && (!fix || mbar_wait(&mask_full[masks & 1], (masks >> 1) & 1, abort_flag));
       if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-      float f_own = 1.f, f_other = 0.f, M = m_run, l = l_run;
-      if (!it.pair) {
-        // the two tiles of the same rows: each row's (m, l) through shared
-        // memory; then this tile takes half of the columns of both outputs
-        s_ml[t * 128 + row] = make_float2(m_run, l_run);
-        mbar_arrive(&both[0]);
-        w_ok = mbar_wait(&both[0], meets & 1, abort_flag) &&
-               (nother == 0 || mbar_wait(&pv_done[t ^ 1], (other - 1) & 1, abort_flag));
-        if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-        const float2 o = s_ml[(t ^ 1) * 128 + row];
-        M = fmaxf(m_run, o.x);
-        const float Mu = M == -INFINITY ? 0.f : M;
-        f_own = mine == 0 ? 0.f : ex2_approx(m_run - Mu);
-        f_other = nother == 0 ? 0.f : ex2_approx(o.x - Mu);
-        l = (mine == 0 ? 0.f : f_own * l_run) + (nother == 0 ? 0.f : f_other * o.y);
-      }
       tc_fence_after();
       const bool whole = it.whole();
-      const bool live = row < nrow;
-      const float inv = whole ? 1.f / l : 1.f;
-      const uint32_t part = (2 * cta + (it.j0 == 0 ? 1 : 0)) * P.prow + (it.pair ? t * 128 : 0) + row;
-      uint4 mk = make_uint4(0u, 0u, 0u, 0u);
-      bool any_bad = false;
-      if (it.has_drafts()) {
-        // (waited for already by the tile whose block it was)
-        if (!mbar_wait(&mask_full[masks & 1], (masks >> 1) & 1, abort_flag)) { ok = false; }
-        const uint4 bd = *reinterpret_cast<const uint4*>(s_bad + (masks & 1) * 4);
-        mk = s_mask[(masks & 1) * kTreeMax + tok];
-        mk = make_uint4(mk.x & bd.x, mk.y & bd.y, mk.z & bd.z, mk.w & bd.w);
-        any_bad = (mk.x | mk.y | mk.z | mk.w) != 0u;
+      // what a thread writes: columns c0 .. c0 + nc - 1 of either half of row `wrow`
+      int wrow = row, c0 = 0, nc = 32, wslot = slot, wtok = tok;
+      size_t wout = out;
+      float M = m_run, l = l_run, f = 1.f;
+      if (!it.pair) {
+        // tiles and copies are added through shared memory: (m, l) of each,
+        // then each O scaled to the common maximum
+        s_ml[t * 128 + row] = make_float2(m_run, l_run);
+        if (!(ok = meet())) break;  // (Q of both tiles is no longer read, either)
+        float Mx = -INFINITY;
+        for (int i = row % width; i < 256; i += width) Mx = fmaxf(Mx, s_ml[i].x);
+        f = mine == 0 ? 0.f : ex2_approx(m_run - (Mx == -INFINITY ? 0.f : Mx));
+        // 256 threads over `width` rows: 256 / width threads a row
+        const int tix = t * 128 + row, per = 256 / width;
+        wrow = tix / per;
+        nc = 32 / per;  // of each half
+        c0 = (tix % per) * nc;
+        M = -INFINITY;
+        for (int i = wrow; i < 256; i += width) M = fmaxf(M, s_ml[i].x);
+        l = 0.f;
+        for (int i = wrow; i < 256; i += width) {
+          const float2 ml = s_ml[i];
+          // (a tile without blocks has m = -inf, l = 0)
+          l += ml.y * (ml.y == 0.f ? 0.f : ex2_approx(ml.x - (M == -INFINITY ? 0.f : M)));
+        }
+        const int wc = min(base + wrow, it.R - 1);
+        wtok = tree_row_token(wc, it.n, p.k);
+        wslot = tree_row_slot(wc, it.n, it.g, p.k, p.G);
+        wout = ((size_t)it.b * p.T + wtok) * p.Ha + wslot;
       }
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      if (warp_on) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!it.pair && h != t) continue;
-          float o[32];
-          {
+      const bool live = wrow < nrow;
+      const float inv = whole ? 1.f / l : 1.f;
+      const uint32_t part = (2 * cta + (it.j0 == 0 ? 1 : 0)) * p.prow + (it.pair ? t * 128 : 0) + wrow;
+      uint4 mk = make_uint4(0u, 0u, 0u, 0u);
+      if (fix) {
+        const uint4 bd = *reinterpret_cast<const uint4*>(s_bad + (masks & 1) * 4);
+        mk = s_mask[(masks & 1) * kTreeMax + wtok];
+        mk = make_uint4(mk.x & bd.x, mk.y & bd.y, mk.z & bd.z, mk.w & bd.w);
+      }
+      const bool any_bad = (mk.x | mk.y | mk.z | mk.w) != 0u;
+      for (int h = 0; h < 2; ++h) {
+        if (!it.pair) {
+          // this half of the columns of every row, scaled
+          if (h == 1 && !(ok = meet())) break;  // (the first half is read)
+          if (warp_on) {
             uint32_t a[32];
-            if (mine > 0) {
-              tmem_ld32(tm_o + h * 32, a);
+            if (mine > 0) tmem_ld32(T.tm_o + h * 32, a);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(a[i]) * f_own;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-            if (!it.pair && nother > 0) {
-              tmem_ld32(tmem_base + lane_off + 256 + (t ^ 1) * 64 + h * 32, a);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(a[i]), f_other, o[i]);
+            for (int i = 0; i < 8; ++i) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (mine > 0)
+                v = make_float4(__uint_as_float(a[4 * i]) * f, __uint_as_float(a[4 * i + 1]) * f,
+                                __uint_as_float(a[4 * i + 2]) * f, __uint_as_float(a[4 * i + 3]) * f);
+              sums[(t * 128 + row) * 8 + (i ^ (row & 7))] = v;
             }
           }
-          if (any_bad && live) {
-            for (int w = 0; w < 4; ++w)
-              for (uint32_t bits = mask_word(mk, w); bits; bits &= bits - 1) {
-                const __nv_bfloat16* v =
-                    p.Vn + (((size_t)it.b * p.T + w * 32 + __ffs(bits) - 1) * p.G + it.g) * 64 + h * 32;
+          if (!(ok = meet())) break;
+        }
+        for (int c = h * 32 + c0; c < h * 32 + c0 + nc; c += kTuPiece) {
+        float o[kTuPiece];
+        if (it.pair) {
+          if (!warp_on) break;
+          uint32_t a[kTuPiece];
+          tmem_ld4(T.tm_o + c, a);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float x = __bfloat162float(v[i]);
-                  if (!isfinite(x)) o[i] += x;
-                }
-              }
-          }
-          if (live && whole) {
-            __nv_bfloat16* dst = p.O + out * 64 + h * 32;
+          for (int i = 0; i < kTuPiece; ++i) o[i] = __uint_as_float(a[i]);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              st_global_v4(dst + i * 8, pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                           pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                           pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                           pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          } else if (live) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (size_t)part * 64 + h * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < kTuPiece; ++i) o[i] = 0.f;
+          for (int i = wrow; i < 256; i += width) {
+            const float4 a = sums[i * 8 + (((c & 31) >> 2) ^ (i & 7))];
+            o[0] += a.x;
+            o[1] += a.y;
+            o[2] += a.z;
+            o[3] += a.w;
           }
         }
+        if (any_bad && live) {
+          for (int w = 0; w < 4; ++w)
+            for (uint32_t bits = mask_word(mk, w); bits; bits &= bits - 1) {
+              const __nv_bfloat16* v = p.Vn + (((size_t)it.b * p.T + w * 32 + __ffs(bits) - 1) * p.G + it.g) * 64 + c;
+#pragma unroll
+              for (int i = 0; i < kTuPiece; ++i) {
+                const float x = __bfloat162float(v[i]);
+                if (!isfinite(x)) o[i] += x;
+              }
+            }
+        }
+        if (live && whole)
+          *reinterpret_cast<uint2*>(p.O + wout * 64 + c) =
+              make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+        else if (live)
+          *reinterpret_cast<float4*>(p.part_o + (size_t)part * 64 + c) = make_float4(o[0], o[1], o[2], o[3]);
+        }
       }
-      if (live && (it.pair || t == 0)) {
+      if (!ok) break;
+      if (live && c0 == 0) {
         if (!whole)
           *reinterpret_cast<float2*>(p.part_ml + (size_t)part * 2) = make_float2(M, l);
         else if (p.lse)
-          p.lse[out] = (M + log2f(l)) * 0.6931471805599453f;
+          p.lse[wout] = (M + log2f(l)) * 0.6931471805599453f;
       }
       if (t == 0 && row == 0 && it.j0 == 0) {
         // the ranges that hold blocks of this unit
         const long long ubase = cur.base - (long long)it.nblk * tu_weight(it.rows);
-        P.unit_cta[it.unit] =
-            make_int2(cta, tu_range_of(total, grid, ubase + (long long)(it.nblk - 1) * tu_weight(it.rows)));
+        p.unit_cta[it.unit] =
+            make_int2(cta, tree_range_of(total, grid, ubase + (long long)(it.nblk - 1) * tu_weight(it.rows)) * step +
+                               (step > 1 ? cta % step : 0));
       }
       tc_fence_before();
-      if (it.has_drafts()) {
+      if (fix) {
         mbar_arrive(&mask_empty[masks & 1]);
         ++masks;
       }
-      if (!it.pair) {
-        // neither tile's next O may overwrite what the other still reads
-        mbar_arrive(&both[1]);
-        w_ok = mbar_wait(&both[1], meets & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-        ++meets;
-      }
+      // the sums are read: the next unit's Q may take their place
+      if (!it.pair && !(ok = meet())) break;
       kv += nj;
     }
   }
@@ -701,80 +823,6 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
-}
-
-// The parts of every row that was cut, added: `kParts` groups of 16 lanes a row,
-// four dimensions a lane.
-constexpr int kTuMergeThreads = 128;
-template <int kParts>
-__global__ void __launch_bounds__(kTuMergeThreads) tree_umma_merge_kernel(const TreeUmmaParams P) {
-  static_assert(kParts == 2 || kParts == 8, "a warp or the block per row");
-  const TreeParams& p = P.p;
-  __shared__ float s_m[kTuMergeThreads / 16], s_l[kTuMergeThreads / 16];
-  __shared__ float4 s_o[kTuMergeThreads];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, part = (tid >> 4) % kParts, d = tid & 15;
-  constexpr int kRowsPer = kTuMergeThreads / 16 / kParts;
-  const int sub = (tid >> 4) / kParts;
-  const long long id = (long long)blockIdx.x * kRowsPer + sub;
-  bool on = id < (long long)p.B * p.T * p.Ha;
-  const long long cid = on ? id : 0;
-  const int slot = (int)(cid % p.Ha), bt = (int)(cid / p.Ha), b = bt / p.T, tok = bt % p.T;
-  int L, n;
-  tree_lens(p.cache_len, p.draft_len, b, p.cap, p.T, L, n);
-  on = on && tok < n;
-  const bool shared = slot == p.G * p.k;
-  const int g = shared ? 0 : slot / p.k;
-  const int row = shared ? n * p.k + tok : tok * p.k + slot % p.k;
-  const int s = row / kTuRows;
-  int2 ctas = make_int2(0, 0);
-  if (on) ctas = P.unit_cta[b * (P.u0 + (p.G - 1) * P.u1) + (g == 0 ? s : P.u0 + (g - 1) * P.u1 + s)];
-  on = on && ctas.x != ctas.y;  // (else it was written at once)
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (on) {
-    for (int c = ctas.x + part; c <= ctas.y; c += kParts) {
-      const size_t at = (size_t)(2 * c + (c == ctas.x ? 1 : 0)) * P.prow + row % kTuRows;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * 64 + d * 4);
-      const float M = fmaxf(m, ml.x), Mu = M == -INFINITY ? 0.f : M;
-      const float f0 = ex2_approx(m - Mu), f1 = ex2_approx(ml.x - Mu);
-      m = M;
-      l = fmaf(l, f0, ml.y * f1);
-      o.x = fmaf(o.x, f0, v.x * f1);
-      o.y = fmaf(o.y, f0, v.y * f1);
-      o.z = fmaf(o.z, f0, v.z * f1);
-      o.w = fmaf(o.w, f0, v.w * f1);
-    }
-  }
-  if (d == 0) {
-    s_m[tid >> 4] = m;
-    s_l[tid >> 4] = l;
-  }
-  s_o[tid] = o;
-  __syncthreads();
-  if (!on || part != 0) return;
-  float M = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < kParts; ++q) M = fmaxf(M, s_m[sub * kParts + q]);
-  const float Mu = M == -INFINITY ? 0.f : M;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll
-  for (int q = 0; q < kParts; ++q) {
-    const float f = ex2_approx(s_m[sub * kParts + q] - Mu);
-    const float4 v = s_o[(sub * kParts + q) * 16 + d];
-    sum = fmaf(s_l[sub * kParts + q], f, sum);
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
-  }
-  const float inv = 1.f / sum;
-  const size_t out = (size_t)bt * p.Ha + slot;
-  *reinterpret_cast<uint2*>(p.O + out * 64 + d * 4) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (p.lse && d == 0) p.lse[out] = (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace gqe

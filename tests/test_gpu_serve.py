@@ -181,16 +181,18 @@ def run_tree(d, cap, v, O=None, lse=None, ws=None, with_lse=True):
     return O, lse
 
 
-def check_tree(d, x, O, lse):
+def check_tree(d, x, O, lse, only=slice(None)):
     want = ref.tree_attn(x["Q"], x["Kn"], x["Vn"], x["Kc"], x["Vc"], x["lens"].numpy(),
                          None if x["drafts"] is None else x["drafts"].numpy(),
                          None if x["parent"] is None else x["parent"].numpy(), d.B, d.T, d.G, d.k)
-    live = ~np.isnan(want["lse"])
+    live = np.zeros(want["lse"].shape, bool)
+    live[only] = ~np.isnan(want["lse"][only])
     s = 2.0 ** -17 * want["score"]
     tol = HALF * (np.abs(want["O"]) + want["terms"]) + (2 * s + 2.0 ** -14)[..., None] * want["terms"]
     within(f64(O)[live], want["O"][live], tol[live], "O")
     within(f64(lse)[live], want["lse"][live], (s + 2.0 ** -20 * (1 + np.abs(want["lse"])))[live], "lse")
-    assert (f64(O)[~live] == 7.0).all() and (f64(lse)[~live] == 7.0).all(), "rows past draft_len changed"
+    dead = np.isnan(want["lse"])
+    assert (f64(O)[dead] == 7.0).all() and (f64(lse)[dead] == 7.0).all(), "rows past draft_len changed"
 
 
 TREE = [
@@ -278,8 +280,9 @@ def test_tree_out_of_range_lengths_and_parents_are_reported():
         O2, lse2 = run_tree(d, 50, w)
         assert gqe.gqe_check_error() == -7
         assert (O2[6:12] == 7.0).all() and (lse2[6:12] == 7.0).all()
+        # (the others' keys may be cut into other ranges: the same up to rounding)
         for rows in (slice(0, 6), slice(12, 24)):
-            assert torch.equal(O2[rows], O[rows]) and torch.equal(lse2[rows], lse[rows])
+            check_tree(d, x, O2, lse2, only=rows)
     for bad in (3, 5, -2, 2 ** 31 - 1):
         w = dict(v, parent=v["parent"].clone())
         w["parent"][6 + 3] = bad  # token 3 of sequence 1: its own index, a later one, below -1
