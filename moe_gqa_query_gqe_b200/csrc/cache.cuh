@@ -19,7 +19,6 @@ struct CommitParams {
   float* mass_out;
   int32_t* new_len;
   int B, T, G, k, Ha, cap;
-  int nsplit;  // blocks of one (sequence, group) in the mass kernel
   float scale_log2;
 };
 
@@ -44,8 +43,26 @@ __device__ __forceinline__ int commit_token(const CommitParams& p, int b, int j)
   return i;
 }
 
-// Accepted rows into the cache: one block per (sequence, place of the path),
-// G*64 values of K and of V, and the G positions.
+// Place j of sequence b's accepted path into the cache, by `threads` threads of
+// which this is `i`: G*64 values of K and of V, and the G positions.
+__device__ __forceinline__ void commit_append_row(const CommitParams& p, int b, int j, int L, int n, int i, int threads) {
+  if (j == 0 && i == 0) p.new_len[b] = n < 0 ? p.cache_len[b] : L + n;
+  if (j >= n) return;
+  const int tok = commit_token(p, b, j);
+  if (tok < 0) return;
+  const size_t src = ((size_t)b * p.T + tok) * p.G * 64, dst = ((size_t)b * p.cap + L + j) * p.G * 64;
+  for (int t = i; t < p.G * 16; t += threads) {
+    const int at = (t >> 1) * 8;
+    const __nv_bfloat16* s = (t & 1 ? p.Vn : p.Kn) + src + at;
+    __nv_bfloat16* d = (t & 1 ? p.Vc : p.Kc) + dst + at;
+    *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+  }
+  if (p.pos != nullptr)
+    for (int g = i; g < p.G; g += threads)
+      p.pos[((size_t)b * p.G + g) * p.cap + L + j] = p.positions ? p.positions[(size_t)b * p.T + tok] : L + j;
+}
+
+// The commit without the sums: one block per (sequence, place of the path).
 constexpr int kAppendThreads = 128;
 __global__ void __launch_bounds__(kAppendThreads) commit_append_kernel(const CommitParams p) {
   pdl_wait();
@@ -53,137 +70,7 @@ __global__ void __launch_bounds__(kAppendThreads) commit_append_kernel(const Com
   const int b = blockIdx.x / p.T, j = blockIdx.x % p.T;
   int L, n;
   commit_lens(p, b, L, n);
-  if (j == 0 && threadIdx.x == 0) p.new_len[b] = n < 0 ? p.cache_len[b] : L + n;
-  if (j >= n) return;
-  const int i = commit_token(p, b, j);
-  if (i < 0) return;
-  const size_t src = ((size_t)b * p.T + i) * p.G * 64, dst = ((size_t)b * p.cap + L + j) * p.G * 64;
-  for (int t = threadIdx.x; t < p.G * 16; t += kAppendThreads) {
-    const int at = (t >> 1) * 8;
-    const __nv_bfloat16* s = (t & 1 ? p.Vn : p.Kn) + src + at;
-    __nv_bfloat16* d = (t & 1 ? p.Vc : p.Kc) + dst + at;
-    *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
-  }
-  if (p.pos != nullptr)
-    for (int g = threadIdx.x; g < p.G; g += kAppendThreads)
-      p.pos[((size_t)b * p.G + g) * p.cap + L + j] = p.positions ? p.positions[(size_t)b * p.T + i] : L + j;
-}
-
-// mass_out[s] = mass_in[s] (0 for the new rows) + sum over the accepted tokens
-// j and the rows of each, s <= L + j, of exp(q.k_s / 8 - lse).
-//
-// The scores are taken transposed, S^T = K Q^T (mma.sync m16n8k16): a warp
-// holds 16 keys as the A operand in registers, for all query rows, so a key's
-// sum runs along one thread's fragments and needs two shuffles at the end. The
-// rows' lse are subtracted in the exponent. The 64 keys of a block's step are
-// read once, straight into fragments.
-constexpr int kMassThreads = 128;
-constexpr int kMassKeys = 64;
-constexpr int kMassRows = 128;  // query rows staged at a time
-__global__ void __launch_bounds__(kMassThreads) cache_mass_mma_kernel(const CommitParams p) {
-  __shared__ __align__(1024) uint8_t s_q[kMassRows * 128];
-  __shared__ float s_lse[kMassRows];
-  __shared__ int s_lim[kMassRows];  // last position the row attends
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bg = blockIdx.x / p.nsplit, split = blockIdx.x % p.nsplit;
-  const int b = bg / p.G, g = bg % p.G;
-  int L, n;
-  commit_lens(p, b, L, n);
-  if (n < 0) return;
-  const int keys = L + n;
-  const int nblk = (keys + kMassKeys - 1) / kMassKeys;
-  const int j0 = (int)((long long)nblk * split / p.nsplit), j1 = (int)((long long)nblk * (split + 1) / p.nsplit);
-  if (j0 >= j1) return;
-  const int R = n * (p.k + (g == 0 ? 1 : 0));
-  const int nchunk = (R + kMassRows - 1) / kMassRows;
-  const int r = lane >> 2, c = lane & 3;
-  const int mi = lane >> 3, mr = lane & 7;
-  const uint32_t qb = smem_u32(s_q);
-  auto stage = [&](int chunk) {
-    for (int i = tid; i < kMassRows * 8; i += kMassThreads) {
-      const int row = i >> 3, ch = i & 7, at = chunk * kMassRows + row;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (at < R) {
-        const int tok = commit_token(p, b, tree_row_token(at, n, p.k));
-        const int slot = tree_row_slot(at, n, g, p.k, p.G);
-        const size_t qrow = ((size_t)b * p.T + max(tok, 0)) * p.Ha + slot;
-        if (tok >= 0) v = reinterpret_cast<const uint4*>(p.Q + qrow * 64)[ch];
-        if (ch == 0) {
-          s_lse[row] = tok >= 0 ? p.lse[qrow] * 1.4426950408889634f : 0.f;
-          s_lim[row] = tok >= 0 ? L + tree_row_token(at, n, p.k) : -1;
-        }
-      } else if (ch == 0) {
-        s_lse[row] = 0.f;
-        s_lim[row] = -1;
-      }
-      *reinterpret_cast<uint4*>(s_q + row * 128 + ((ch ^ (row & 7)) << 4)) = v;
-    }
-  };
-  if (nchunk == 1) {
-    stage(0);
-    __syncthreads();
-  }
-  for (int j = j0; j < j1; ++j) {
-    // this thread's keys: rows r and r + 8 of the warp's 16
-    const int ka = j * kMassKeys + warp * 16 + r, kb = ka + 8;
-    uint32_t a[4][4];
-    auto key_row = [&](int s) -> const __nv_bfloat16* {
-      if (s < L) return p.Kc + (((size_t)b * p.cap + s) * p.G + g) * 64;
-      const int tok = s < keys ? commit_token(p, b, s - L) : -1;
-      return tok < 0 ? nullptr : p.Kn + (((size_t)b * p.T + tok) * p.G + g) * 64;
-    };
-    const __nv_bfloat16 *k0 = key_row(ka), *k1 = key_row(kb);
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const int d0 = 16 * kk + 2 * c;
-      a[kk][0] = k0 ? *reinterpret_cast<const uint32_t*>(k0 + d0) : 0u;
-      a[kk][1] = k1 ? *reinterpret_cast<const uint32_t*>(k1 + d0) : 0u;
-      a[kk][2] = k0 ? *reinterpret_cast<const uint32_t*>(k0 + d0 + 8) : 0u;
-      a[kk][3] = k1 ? *reinterpret_cast<const uint32_t*>(k1 + d0 + 8) : 0u;
-    }
-    float sum0 = 0.f, sum1 = 0.f;
-    const bool all = (j + 1) * kMassKeys <= L;  // every row attends every key of the block
-    for (int chunk = 0; chunk < nchunk; ++chunk) {
-      if (nchunk > 1) {
-        __syncthreads();
-        stage(chunk);
-        __syncthreads();
-      }
-      const int rows = min(kMassRows, R - chunk * kMassRows);
-      for (int q0 = 0; q0 < rows; q0 += 16) {
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const int row = q0 + (mi >> 1) * 8 + mr, ch = 2 * kk + (mi & 1);
-          uint32_t b0, b1, b2, b3;
-          ldsm_x4(qb + row * 128 + ((ch ^ (row & 7)) << 4), b0, b1, b2, b3);
-          mma_bf16_16816(s[0], a[kk], b0, b1);
-          mma_bf16_16816(s[1], a[kk], b2, b3);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = q0 + h * 8 + 2 * c + e;
-            const float ls = s_lse[row];
-            const int lim = s_lim[row];
-            const float e0 = ex2_approx(fmaf(s[h][e], p.scale_log2, -ls));
-            const float e1 = ex2_approx(fmaf(s[h][2 + e], p.scale_log2, -ls));
-            if (all ? lim >= 0 : ka <= lim) sum0 += e0;
-            if (all ? lim >= 0 : kb <= lim) sum1 += e1;
-          }
-      }
-    }
-    sum0 += __shfl_xor_sync(0xffffffffu, sum0, 1);
-    sum0 += __shfl_xor_sync(0xffffffffu, sum0, 2);
-    sum1 += __shfl_xor_sync(0xffffffffu, sum1, 1);
-    sum1 += __shfl_xor_sync(0xffffffffu, sum1, 2);
-    const size_t at = ((size_t)b * p.G + g) * p.cap;
-    if (c == 0 && ka < keys) p.mass_out[at + ka] = (ka < L ? p.mass_in[at + ka] : 0.f) + sum0;
-    if (c == 0 && kb < keys) p.mass_out[at + kb] = (kb < L ? p.mass_in[at + kb] : 0.f) + sum1;
-  }
+  commit_append_row(p, b, j, L, n, threadIdx.x, kAppendThreads);
 }
 
 // ---------------------------------------------------------------------------

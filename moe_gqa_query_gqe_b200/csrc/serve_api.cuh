@@ -4,6 +4,7 @@
 #pragma once
 
 #include "cache.cuh"
+#include "mass.cuh"
 #include "rope.cuh"
 #include "tree.cuh"
 #include "tree_umma.cuh"
@@ -260,11 +261,20 @@ int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path, const i
   p.Ha = d->G * d->k + 1;
   p.cap = cap;
   p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
-  GQE_TRY(launch_pdl(commit_append_kernel, dim3((unsigned)(d->B * d->T)), dim3(kAppendThreads), 0, st, p));
-  if (mass_in == nullptr) return GQE_OK;
-  const long long bg = (long long)d->B * d->G;
-  p.nsplit = (int)std::min<long long>(cdiv(cap, kMassKeys), std::max<long long>(1, cdiv(148 * 8, bg)));
-  return launch_pdl(cache_mass_mma_kernel, dim3((unsigned)(bg * p.nsplit)), dim3(kMassThreads), 0, st, p);
+  if (mass_in == nullptr)
+    return launch_pdl(commit_append_kernel, dim3((unsigned)(d->B * d->T)), dim3(kAppendThreads), 0, st, p);
+  MassParams P;
+  memset(&P, 0, sizeof(P));
+  P.c = p;
+  GQE_TRY(tmap_heads(&P.tmK, K_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
+  const int rows = d->T * (d->k + 1);
+  P.nchunk = (int)cdiv(rows, 128);
+  P.nstage = kMassMaxStages;
+  while (mass_smem(P.nchunk, P.nstage) > 232448) P.nstage -= 2;
+  P.step = rows <= 90 ? d->G : 1;
+  const int smem = mass_smem(P.nchunk, P.nstage);
+  GQE_TRY(set_smem(cache_mass_kernel, smem));
+  return launch_pdl(cache_mass_kernel, dim3((unsigned)(kTreeSms / P.step * P.step)), dim3(kMassThreads), smem, st, P);
 }
 
 int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink, int32_t recent, const int32_t* cache_len,

@@ -59,9 +59,29 @@ __device__ __forceinline__ void tree_lens(const int32_t* cache_len, const int32_
 // into ranges of equal weight; prefix[b] is the weight before sequence b. Every
 // thread of the block calls it, with w(b) the weight of sequence b.
 constexpr int kTreeMaxB = 1024;  // B * G * M <= 8192 and G * M >= 8
+// prefix[1 .. B] to its inclusive sums, by doubling; prefix[0] = 0 before.
+template <int kThreads, typename I>
+__device__ __forceinline__ void scan_prefix(I* prefix, int B) {
+  constexpr int kEach = (kTreeMaxB + kThreads - 1) / kThreads;
+  const int tid = threadIdx.x;
+  for (int d = 1; d < B; d *= 2) {
+    I v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int b = tid + i * kThreads;
+      if (b < B) v[i] = prefix[b + 1] + (b >= d ? prefix[b + 1 - d] : I(0));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int b = tid + i * kThreads;
+      if (b < B) prefix[b + 1] = v[i];
+    }
+    __syncthreads();
+  }
+}
 template <int kThreads, typename I, typename F>
 __device__ __forceinline__ void tree_prefix(const TreeParams& p, I* prefix, F w) {
-  constexpr int kEach = (kTreeMaxB + kThreads - 1) / kThreads;
   const int tid = threadIdx.x;
   if (tid == 0) prefix[0] = 0;
   for (int b = tid; b < p.B; b += kThreads) {
@@ -70,21 +90,7 @@ __device__ __forceinline__ void tree_prefix(const TreeParams& p, I* prefix, F w)
     prefix[b + 1] = n == 0 ? 0 : w(L, n);
   }
   __syncthreads();
-  for (int d = 1; d < p.B; d *= 2) {
-    I v[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int b = tid + i * kThreads;
-      if (b < p.B) v[i] = prefix[b + 1] + (b >= d ? prefix[b + 1 - d] : I(0));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int b = tid + i * kThreads;
-      if (b < p.B) prefix[b + 1] = v[i];
-    }
-    __syncthreads();
-  }
+  scan_prefix<kThreads>(prefix, p.B);
 }
 // The last sequence that begins at or before x.
 template <typename I>
@@ -485,8 +491,8 @@ __global__ void __launch_bounds__(kTreeMergeThreads) tree_merge_kernel(const Tre
   static_assert(kParts == 2 || kParts == 8, "a warp or the block per row");
   __shared__ float s_m[kTreeMergeThreads / 16], s_l[kTreeMergeThreads / 16];
   __shared__ float4 s_o[kTreeMergeThreads];
-  pdl_wait();
-  pdl_trigger();
+  // (The lengths were there before the attention kernel began, and this one
+  // begins when all of its blocks have: they are read before the wait for it.)
   const int tid = threadIdx.x, part = (tid >> 4) % kParts, d = tid & 15;
   constexpr int kRowsPer = kTreeMergeThreads / 16 / kParts;
   const int sub = (tid >> 4) / kParts;
@@ -501,6 +507,8 @@ __global__ void __launch_bounds__(kTreeMergeThreads) tree_merge_kernel(const Tre
   const int g = shared ? 0 : slot / p.k;
   const int row = shared ? n * p.k + tok : tok * p.k + slot % p.k;
   const int s = row / p.urows;
+  pdl_wait();
+  pdl_trigger();
   int2 ctas = make_int2(0, 0);
   if (on) ctas = p.unit_cta[b * (p.u0 + (p.G - 1) * p.u1) + (g == 0 ? s : p.u0 + (g - 1) * p.u1 + s)];
   on = on && ctas.x != ctas.y;  // (else it was written at once)

@@ -15,7 +15,7 @@
 //   a unit of more than 128 rows   A and B hold its two row tiles, and every
 //                                  K/V block serves both;
 //   else                           A and B hold the same rows and take the
-//                                  blocks in turn, A the even, B the odd ones.
+//                                  range's blocks in turn.
 //                                  With 64 rows or fewer a tile holds them
 //                                  twice, with 32 or fewer four times: each
 //                                  copy takes its half or quarter of the block's
@@ -25,7 +25,7 @@
 // A pair block costs half again what a block of the second kind does (weights 3
 // and 2): it is bound by exponentials, the other by the cache's bytes.
 //
-//   warp 0      TMA producer: K/V blocks through a ring of kTuStages
+//   warp 0      TMA producer: K and V blocks, each through a ring of its own
 //   warps 1, 2  lane 0 issues the MMAs of tile A (warp 1, also the TMEM owner)
 //               or B: S = Q K^T (SS, 128x128x64) and O += P V (TS, N = 64)
 //   warp 3      for a unit's draft block: the ancestor masks, by pointer
@@ -47,7 +47,10 @@
 
 namespace gqe {
 
-constexpr int kTuStages = 5;
+// Stages of K and of V (held longer: until P V). Both even: outside pairs the
+// tiles take turns at the blocks, and so a stage's blocks all belong to one
+// tile, which sees its phases one by one.
+constexpr int kTuKStages = 4, kTuVStages = 6;
 constexpr int kTuThreads = 384;
 constexpr int kTuRegsLow = 88, kTuRegsHigh = 208;  // 88*128 + 208*256 = 168*384
 constexpr int kTuBlock = 128;                      // keys of a block
@@ -63,8 +66,9 @@ struct TreeUmmaParams {
 struct TuSmem {
   static constexpr int kQ = 0;                               // Q_A, Q_B
   static constexpr int kSum = 0;                             // [256][32] fp32: half of both tiles' O, at a unit's end
-  static constexpr int kKV = 32768;                          // stages of K, V
-  static constexpr int kMask = kKV + kTuStages * 32768;      // [2][128] ancestor masks
+  static constexpr int kK = 32768;                           // stages of K
+  static constexpr int kV = kK + kTuKStages * 16384;         // stages of V
+  static constexpr int kMask = kV + kTuVStages * 16384;      // [2][128] ancestor masks
   static constexpr int kUp = kMask + 2 * kTreeMax * 16;      // [128] pointers of the doubling
   static constexpr int kBad = kUp + kTreeMax * 4;            // [2][4] drafts with values that are not finite
   static constexpr int kML = kBad + 32;                      // [2][128] m, l of the tiles
@@ -80,10 +84,6 @@ struct TuItem {
   bool pair;           // two row tiles
   int nblk, j0, j1;    // blocks of the unit; this range's
   int unit;
-  __device__ __forceinline__ int tile_blocks(int t) const {
-    if (pair) return j1 - j0;
-    return (j1 - j0 + 1 - t) >> 1;
-  }
   __device__ __forceinline__ int copies() const { return rows > 64 ? 1 : (rows > 32 ? 2 : 4); }
   __device__ __forceinline__ int row_base(int t) const { return s * kTuRows + (pair ? t * 128 : 0); }
   __device__ __forceinline__ bool has_drafts() const { return j1 == nblk; }
@@ -323,11 +323,11 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBar);
-  uint64_t* k_full = bars;                  // [kTuStages]
-  uint64_t* v_full = k_full + kTuStages;    // [kTuStages]
-  uint64_t* k_empty = v_full + kTuStages;   // [kTuStages] two arrivals: each tile's, or two of the tile whose block it is
-  uint64_t* v_empty = k_empty + kTuStages;  // [kTuStages]
-  uint64_t* q_full = v_empty + kTuStages;   // [2] tiles
+  uint64_t* k_full = bars;                   // [kTuKStages]
+  uint64_t* v_full = k_full + kTuKStages;    // [kTuVStages]
+  uint64_t* k_empty = v_full + kTuVStages;   // [kTuKStages] two arrivals: each tile's, or two of the tile whose block it is
+  uint64_t* v_empty = k_empty + kTuKStages;  // [kTuVStages]
+  uint64_t* q_full = v_empty + kTuVStages;   // [2] tiles
   uint64_t* s_full = q_full + 2;            // [2]
   uint64_t* s_free = s_full + 2;            // [2]
   uint64_t* p_full = s_free + 2;            // [2]
@@ -344,10 +344,12 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int s = 0; s < kTuStages; ++s) {
+    for (int s = 0; s < kTuKStages; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&v_full[s], 1);
       mbar_init(&k_empty[s], 2);
+    }
+    for (int s = 0; s < kTuVStages; ++s) {
+      mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
@@ -410,13 +412,13 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           Stream& a = str[v];
-          const int s = a.n % kTuStages;
-          if (a.done || !mbar_test(v ? &v_empty[s] : &k_empty[s], ((a.n / kTuStages) & 1) ^ 1)) continue;
+          const uint32_t stages = v ? kTuVStages : kTuKStages, s = a.n % stages;
+          if (a.done || !mbar_test(v ? &v_empty[s] : &k_empty[s], ((a.n / stages) & 1) ^ 1)) continue;
           const bool drafts = a.j == a.it.nblk - 1;
           const int row = drafts ? a.it.b * p.T : a.it.b * p.cap + a.j * kTuBlock;
           uint64_t* full = v ? &v_full[s] : &k_full[s];
           mbar_arrive_expect_tx(full, 16384);
-          tma_load_3d(smem + S::kKV + s * 32768 + v * 16384, v ? (drafts ? &P.tmVn : &P.tmV) : (drafts ? &P.tmKn : &P.tmK),
+          tma_load_3d(smem + (v ? S::kV : S::kK) + s * 16384, v ? (drafts ? &P.tmVn : &P.tmV) : (drafts ? &P.tmKn : &P.tmK),
                       full, 0, a.it.g, row);
           ++a.n;
           moved = true;
@@ -447,32 +449,33 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       bool ok = true;
       const uint32_t qa = sbase + S::kQ + t * 16384;
       auto s_ready = [&](uint32_t kvi) {
-        return mbar_test(&k_full[kvi % kTuStages], (kvi / kTuStages) & 1) &&
+        return mbar_test(&k_full[kvi % kTuKStages], (kvi / kTuKStages) & 1) &&
                (s_cnt == 0 || mbar_test(&s_free[t], (s_cnt - 1) & 1));
       };
       auto issue_s = [&](uint32_t kvi, bool alone) {  // (ready)
         tc_fence_after();
-        const uint32_t ka = sbase + S::kKV + (kvi % kTuStages) * 32768;
+        const uint32_t ka = sbase + S::kK + (kvi % kTuKStages) * 16384;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_ss(tmem_base + t * 128, sdesc_sw128(qa + kk * 32, 16, 1024), sdesc_sw128(ka + kk * 32, 16, 1024), idesc_s,
                   kk != 0);
         umma_commit(&s_full[t]);
-        umma_commit(&k_empty[kvi % kTuStages]);
-        if (alone) umma_commit(&k_empty[kvi % kTuStages]);
+        umma_commit(&k_empty[kvi % kTuKStages]);
+        if (alone) umma_commit(&k_empty[kvi % kTuKStages]);
         ++s_cnt;
       };
       auto wait_s = [&](uint32_t kvi) {
-        return mbar_wait(&k_full[kvi % kTuStages], (kvi / kTuStages) & 1, abort_flag) &&
+        return mbar_wait(&k_full[kvi % kTuKStages], (kvi / kTuKStages) & 1, abort_flag) &&
                (s_cnt == 0 || mbar_wait(&s_free[t], (s_cnt - 1) & 1, abort_flag));
       };
       while (ok && cur.next(P, it)) {
         const int nj = it.j1 - it.j0;
-        const int stride = it.pair ? 1 : 2, first = it.pair ? 0 : t;
-        if (!(ok = mbar_wait(&q_full[t], q_cnt & 1, abort_flag))) break;
-        ++q_cnt;
+        const int stride = it.pair ? 1 : 2, first = it.pair ? 0 : (int)((kv & 1) ^ t);
+        // (q_full counts the units that have a block of this tile: in the others
+        // neither side waits for the other, and their phases could drift apart)
         if (first < nj) {
-          if (!(ok = wait_s(kv + first))) break;
+          if (!(ok = mbar_wait(&q_full[t], q_cnt & 1, abort_flag) && wait_s(kv + first))) break;
+          ++q_cnt;
           issue_s(kv + first, !it.pair);
         }
         for (int jj = first; jj < nj; jj += stride) {
@@ -489,17 +492,17 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
             }
           }
           if (!(ok = mbar_wait(&p_full[t], pv_cnt & 1, abort_flag))) break;
-          if (!(ok = mbar_wait(&v_full[kvj % kTuStages], (kvj / kTuStages) & 1, abort_flag))) break;
+          if (!(ok = mbar_wait(&v_full[kvj % kTuVStages], (kvj / kTuVStages) & 1, abort_flag))) break;
           tc_fence_after();
-          const uint32_t va = sbase + S::kKV + (kvj % kTuStages) * 32768 + 16384;
+          const uint32_t va = sbase + S::kV + (kvj % kTuVStages) * 16384;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_ts(tmem_base + 256 + t * 64, tmem_base + 384 + t * 64 + kk * 8, sdesc_sw128(va + kk * 2048, 8192, 1024),
                     idesc_o, (jj != first || kk != 0) ? 1u : 0u);
           umma_commit(&pv_done[t]);
           ++pv_cnt;
-          umma_commit(&v_empty[kvj % kTuStages]);
-          if (!it.pair) umma_commit(&v_empty[kvj % kTuStages]);
+          umma_commit(&v_empty[kvj % kTuVStages]);
+          if (!it.pair) umma_commit(&v_empty[kvj % kTuVStages]);
           if (ahead) {
             if (!(ok = wait_s(kvj + stride))) break;
             issue_s(kvj + stride, !it.pair);
@@ -601,6 +604,8 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       return __all_sync(0xffffffffu, w_ok);
     };
     while (ok && cur.next(P, it)) {
+      const int nj = it.j1 - it.j0;
+      const int stride = it.pair ? 1 : 2, first = it.pair ? 0 : (int)((kv & 1) ^ t);
       const int D = it.copies(), width = 128 / D;      // rows a copy has room for
       const int copy = row / width;
       const int base = it.row_base(t), r = base + row % width;
@@ -626,10 +631,8 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
 #pragma unroll
           for (int h = 0; h < 4; ++h) tmem_st16(T.tm_p + h * 16, z);
         }
-        mbar_arrive(&q_full[t]);
+        if (first < nj) mbar_arrive(&q_full[t]);
       }
-      const int nj = it.j1 - it.j0;
-      const int stride = it.pair ? 1 : 2, first = it.pair ? 0 : t;
       float m_run = -INFINITY, l_run = 0.f;
       for (int jj = first; jj < nj; jj += stride, ++cnt) {
         const int j = it.j0 + jj;
@@ -640,8 +643,8 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
           // this thread's value row: zeroed past the last valid one; without
           // the values that are not finite in a drafted row
           const uint32_t kvj = kv + jj;
-          w_ok = mbar_wait(&v_full[kvj % kTuStages], (kvj / kTuStages) & 1, abort_flag);
-          uint8_t* vs = smem + S::kKV + (kvj % kTuStages) * 32768 + 16384 + row * 128;
+          w_ok = mbar_wait(&v_full[kvj % kTuVStages], (kvj / kTuVStages) & 1, abort_flag);
+          uint8_t* vs = smem + S::kV + (kvj % kTuVStages) * 16384 + row * 128;
           if (w_ok && row >= valid) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vs + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
         if (!ok) break;
       }
       if (!ok) break;
-      const int mine = it.tile_blocks(t);
+      const int mine = first < nj ? 1 : 0;  // has blocks
       // ---- the unit's end ------------------------------------------------------------
       bool w_ok = mine == 0 || mbar_wait(&pv_done[t], (cnt - 1) & 1, abort_flag);
       // the drafts that are not finite and their masks (waited for already by
