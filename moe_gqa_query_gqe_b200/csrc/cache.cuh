@@ -84,9 +84,10 @@ struct EvictParams {
   const int32_t* pos_in;
   int32_t* pos_out;
   int32_t* new_len;
-  int32_t *moves;  // [B*G] rows to move
-  int32_t *holes, *late;  // [B*G][cap / 2 + 1] slots left empty below keep, rows kept past it
+  int32_t *holes, *late;  // [B*G][list] slots left empty below keep, rows kept past it
   int B, G, cap, keep, sink, recent, list;
+  int ncta;  // blocks of a cluster
+  int held;  // keys a block can hold in shared memory
 };
 
 // Order of the rows as unsigned numbers: a row that must stay above every
@@ -97,55 +98,113 @@ __device__ __forceinline__ uint32_t evict_key(float m, int pos, int sink, long l
   const uint32_t u = __float_as_uint(m + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ int ld_dsmem_s32(uint32_t cluster_addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 
-// One block per (sequence, group): the keep-th largest key by four 8-bit radix
-// passes over the rows (mass and position, 8 bytes a row, from L2 after the
-// first), then the rows in order: a row stays if its key is larger, or equal
-// and among the first of the equal ones. Mass and position of the staying rows
-// are written; the empty slots below keep and the staying rows past it go to
-// the lists, in order.
-constexpr int kEvictThreads = 1024;
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictParams p) {
-  __shared__ int s_hist[256];
-  __shared__ int s_warp[3][32];
-  __shared__ int s_pick[2];
+// One cluster of `ncta` blocks per (sequence, group). Each block takes a
+// contiguous share of the rows, each warp a contiguous share of the block's, so
+// that (block, warp, step, lane) is the rows' order.
+//   1. Keys (mass and position, 8 bytes a row) are read once and held in shared
+//      memory, as far as they fit.
+//   2. The keep-th largest key by four 8-bit radix passes: a histogram per block,
+//      added over the cluster through distributed shared memory.
+//   3. A row stays if its key is larger, or equal and among the first of the
+//      equal ones; ranks by ballots, then sums over warps and blocks. The empty
+//      slots below keep and the staying rows past it go to two lists, in order.
+//   4. Row j of the one list moves into slot j of the other, eight lanes a row,
+//      K and V, four rows of a lane in flight.
+// Bound by the moved rows' bytes (1 KB a row, read and written), or, where few
+// leave, by the chain of the passes; the blocks of a cluster shorten both.
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictCopies = 4;  // of the histogram, against atomics on one address
+struct EvictShared {
+  int hist[kEvictCopies][256];
+  int total[256];              // this block's histogram: read by the cluster
+  int counts[3];               // equal keys, holes, late rows of this block: read by the cluster
+  int warp[3][kEvictWarps];
+  int pick[2];
+};
+__global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const EvictParams p) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ EvictShared sh;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / p.G;
-  int n = p.cache_len[b];
+  const int bg = blockIdx.x / p.ncta, rank = blockIdx.x % p.ncta, b = bg / p.G, g = bg % p.G;
+  const int n = p.cache_len[b];
+  const bool first = g == 0 && rank == 0 && tid == 0;
   if (n < 0 || n > p.cap) {
     flag_bounds_error();
-    if (tid == 0) p.moves[blockIdx.x] = -1;
+    if (first) p.new_len[b] = n;
     return;
   }
-  const size_t at = (size_t)blockIdx.x * p.cap;
+  if (first) p.new_len[b] = min(n, p.keep);
+  const size_t at = (size_t)bg * p.cap;
   const float* mass = p.mass_in + at;
   const int32_t* pos = p.pos_in + at;
-  const long long recent_from = (long long)p.next_pos[b] - p.recent;
   if (n <= p.keep) {
-    for (int i = tid; i < n; i += kEvictThreads) {
+    for (int i = rank * kEvictThreads + tid; i < n; i += p.ncta * kEvictThreads) {
       p.mass_out[at + i] = mass[i];
       p.pos_out[at + i] = pos[i];
     }
-    if (tid == 0) p.moves[blockIdx.x] = 0;
     return;
   }
+  const long long recent_from = (long long)p.next_pos[b] - p.recent;
+  // this warp's rows: base .. base + len - 1, those below n
+  const int len = ((n + p.ncta - 1) / p.ncta + kEvictThreads - 1) / kEvictThreads * 32;
+  const int share = len * kEvictWarps;
+  const int base = rank * share + warp * len;
+  const bool held = share <= p.held;
+  uint32_t* mine = s_keys + warp * len;
+  auto key_at = [&](int i) -> uint32_t {  // row base + i
+    return held ? mine[i] : evict_key(mass[base + i], pos[base + i], p.sink, recent_from);
+  };
+  const int steps = min(len, max(0, n - base));  // rows of this warp
   uint32_t prefix = 0;
   int need = p.keep;  // rows still to be found among those that share the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
+    for (int i = tid; i < kEvictCopies * 256; i += kEvictThreads) sh.hist[i >> 8][i & 255] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kEvictThreads) {
-      const uint32_t key = evict_key(mass[i], pos[i], p.sink, recent_from);
-      if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&s_hist[(key >> shift) & 255u], 1);
+    int* hist = sh.hist[warp % kEvictCopies];
+    for (int i0 = 0; i0 < steps; i0 += 128) {
+      uint32_t key[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * 32 + lane;
+        if (i < steps)
+          key[u] = shift == 24 ? evict_key(mass[base + i], pos[base + i], p.sink, recent_from) : key_at(i);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * 32 + lane;
+        if (i >= steps) continue;
+        if (shift == 24 && held) mine[i] = key[u];
+        if (shift == 24 || (key[u] >> (shift + 8)) == prefix) atomicAdd(&hist[(key[u] >> shift) & 255u], 1);
+      }
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int v = 0;
+#pragma unroll
+      for (int c = 0; c < kEvictCopies; ++c) v += sh.hist[c][tid];
+      sh.total[tid] = v;
+    }
+    cluster_sync();
+    if (tid < 256) {
+      int v = 0;
+      for (int c = 0; c < p.ncta; ++c) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.total[tid]), c));
+      sh.hist[0][tid] = v;
     }
     __syncthreads();
     if (warp == 0) {
-      // lane l holds bins 8l .. 8l+7; suffix sums from the top
+      // lane l holds bins 8l .. 8l+7; sums from the top
       int bins[8], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += bins[i] = s_hist[lane * 8 + i];
+      for (int i = 0; i < 8; ++i) sum += bins[i] = sh.hist[0][lane * 8 + i];
       int above = sum;
 #pragma unroll
       for (int d = 1; d < 32; d *= 2) {
@@ -155,92 +214,114 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
       above -= sum;  // in the lanes above this one
       for (int i = 7; i >= 0; --i) {
         if (above < need && above + bins[i] >= need) {
-          s_pick[0] = lane * 8 + i;
-          s_pick[1] = need - above;
+          sh.pick[0] = lane * 8 + i;
+          sh.pick[1] = need - above;
         }
         above += bins[i];
       }
     }
-    __syncthreads();
-    prefix = (prefix << 8) | (uint32_t)s_pick[0];
-    need = s_pick[1];
-    __syncthreads();
+    cluster_sync();  // pick is there; every block has read the others' totals
+    prefix = (prefix << 8) | (uint32_t)sh.pick[0];
+    need = sh.pick[1];
   }
-  // the rows in order, 1024 at a time
-  int eq_base = 0, hole_base = 0, late_base = 0;
-  int32_t* holes = p.holes + (size_t)blockIdx.x * p.list;
-  int32_t* late = p.late + (size_t)blockIdx.x * p.list;
-  for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
-    const int i = i0 + tid;
-    float m = 0.f;
-    int ps = 0;
-    uint32_t key = 0;
-    if (i < n) {
-      m = mass[i];
-      ps = pos[i];
-      key = evict_key(m, ps, p.sink, recent_from);
+  // this warp's count of something, summed: over the warps before it and, for the
+  // cluster, over the block (slot `what` of counts)
+  const uint32_t below = (1u << lane) - 1u;
+  auto before = [&](int what) {  // of the cluster's blocks before this one, and this block's warps before this warp
+    int v = 0;
+    for (int w = 0; w < warp; ++w) v += sh.warp[what][w];
+    for (int c = 0; c < rank; ++c) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[what]), c));
+    return v;
+  };
+  auto sum_warps = [&](int what) {
+    if (tid == 0) {
+      int v = 0;
+      for (int w = 0; w < kEvictWarps; ++w) v += sh.warp[what][w];
+      sh.counts[what] = v;
     }
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, i < n && key == prefix);
-    if (lane == 0) s_warp[0][warp] = __popc(eq);
-    __syncthreads();
-    int rank = eq_base, eq_all = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int v = s_warp[0][w];
-      if (w < warp) rank += v;
-      eq_all += v;
+  };
+  int eq = 0;
+  for (int i0 = 0; i0 < steps; i0 += 32) {
+    const int i = i0 + lane;
+    eq += __popc(__ballot_sync(0xffffffffu, i < steps && key_at(i) == prefix));
+  }
+  if (lane == 0) sh.warp[0][warp] = eq;
+  __syncthreads();
+  sum_warps(0);
+  cluster_sync();
+  const int eq0 = before(0);
+  int holes = 0, late = 0;
+  eq = eq0;
+  for (int i0 = 0; i0 < steps; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t key = i < steps ? key_at(i) : 0u;
+    const uint32_t e = __ballot_sync(0xffffffffu, i < steps && key == prefix);
+    const bool stays = i < steps && (key > prefix || (key == prefix && eq + __popc(e & below) < need));
+    eq += __popc(e);
+    holes += __popc(__ballot_sync(0xffffffffu, i < steps && base + i < p.keep && !stays));
+    late += __popc(__ballot_sync(0xffffffffu, base + i >= p.keep && stays));
+  }
+  if (lane == 0) {
+    sh.warp[1][warp] = holes;
+    sh.warp[2][warp] = late;
+  }
+  __syncthreads();
+  sum_warps(1);
+  __syncwarp();
+  sum_warps(2);
+  cluster_sync();
+  holes = before(1);
+  late = before(2);
+  int32_t* hole_list = p.holes + (size_t)bg * p.list;
+  int32_t* late_list = p.late + (size_t)bg * p.list;
+  eq = eq0;
+  for (int i0 = 0; i0 < steps; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t key = i < steps ? key_at(i) : 0u;
+    const uint32_t e = __ballot_sync(0xffffffffu, i < steps && key == prefix);
+    const bool stays = i < steps && (key > prefix || (key == prefix && eq + __popc(e & below) < need));
+    eq += __popc(e);
+    const bool hole = i < steps && base + i < p.keep && !stays, past = base + i >= p.keep && stays;
+    const uint32_t hb = __ballot_sync(0xffffffffu, hole), lb = __ballot_sync(0xffffffffu, past);
+    if (hole) hole_list[holes + __popc(hb & below)] = base + i;
+    if (past) late_list[late + __popc(lb & below)] = base + i;
+    if (stays && !past) {
+      p.mass_out[at + base + i] = mass[base + i];
+      p.pos_out[at + base + i] = pos[base + i];
     }
-    rank += __popc(eq & below);
-    eq_base += eq_all;
-    const bool stays = i < n && (key > prefix || (key == prefix && rank < need));
-    const uint32_t hb = __ballot_sync(0xffffffffu, i < p.keep && !stays);
-    const uint32_t lb = __ballot_sync(0xffffffffu, i >= p.keep && stays);
-    if (lane == 0) {
-      s_warp[1][warp] = __popc(hb);
-      s_warp[2][warp] = __popc(lb);
+    holes += __popc(hb);
+    late += __popc(lb);
+  }
+  int moves = 0;
+  for (int c = 0; c < p.ncta; ++c) moves += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[1]), c));
+  __threadfence();
+  cluster_sync();  // the lists are there; no block's shared memory is read from here on
+  const int l8 = lane & 7;
+  for (int i0 = (rank * kEvictWarps + warp) * 16; i0 < moves; i0 += p.ncta * kEvictWarps * 16) {
+    int to[4], from[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * 4 + (lane >> 3);
+      to[u] = i < moves ? __ldcg(hole_list + i) : -1;
+      from[u] = i < moves ? __ldcg(late_list + i) : 0;
     }
-    __syncthreads();
-    int ho = hole_base, la = late_base, h_all = 0, l_all = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int v = s_warp[1][w], x = s_warp[2][w];
-      if (w < warp) {
-        ho += v;
-        la += x;
+    uint4 kv[4], vv[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (to[u] >= 0) {
+        const size_t src = (((size_t)b * p.cap + from[u]) * p.G + g) * 64;
+        kv[u] = reinterpret_cast<const uint4*>(p.Kc + src)[l8];
+        vv[u] = reinterpret_cast<const uint4*>(p.Vc + src)[l8];
       }
-      h_all += v;
-      l_all += x;
-    }
-    if (i < p.keep && !stays) holes[ho + __popc(hb & below)] = i;
-    if (i >= p.keep && stays) late[la + __popc(lb & below)] = i;
-    if (i < p.keep && stays) {
-      p.mass_out[at + i] = m;
-      p.pos_out[at + i] = ps;
-    }
-    hole_base += h_all;
-    late_base += l_all;
-    __syncthreads();
-  }
-  if (tid == 0) p.moves[blockIdx.x] = hole_base;
-}
-
-// Rows past keep into the holes: eight lanes a row, K and V.
-constexpr int kMoveThreads = 256;
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
-  pdl_wait();
-  pdl_trigger();
-  const int bg = blockIdx.y, b = bg / p.G, g = bg % p.G;
-  const int m = p.moves[bg];
-  if (g == 0 && blockIdx.x == 0 && threadIdx.x == 0) p.new_len[b] = m < 0 ? p.cache_len[b] : min(p.cache_len[b], p.keep);
-  const size_t at = (size_t)bg * p.cap;
-  const int l8 = threadIdx.x & 7;
-  for (int i = blockIdx.x * (kMoveThreads / 8) + (threadIdx.x >> 3); i < m; i += gridDim.x * (kMoveThreads / 8)) {
-    const int to = p.holes[(size_t)bg * p.list + i], from = p.late[(size_t)bg * p.list + i];
-    const size_t src = (((size_t)b * p.cap + from) * p.G + g) * 64, dst = (((size_t)b * p.cap + to) * p.G + g) * 64;
-    const uint4 kv = reinterpret_cast<const uint4*>(p.Kc + src)[l8], vv = reinterpret_cast<const uint4*>(p.Vc + src)[l8];
-    reinterpret_cast<uint4*>(p.Kc + dst)[l8] = kv;
-    reinterpret_cast<uint4*>(p.Vc + dst)[l8] = vv;
-    if (l8 == 0) p.mass_out[at + to] = p.mass_in[at + from];
-    if (l8 == 1) p.pos_out[at + to] = p.pos_in[at + from];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (to[u] >= 0) {
+        const size_t dst = (((size_t)b * p.cap + to[u]) * p.G + g) * 64;
+        reinterpret_cast<uint4*>(p.Kc + dst)[l8] = kv[u];
+        reinterpret_cast<uint4*>(p.Vc + dst)[l8] = vv[u];
+        if (l8 == 0) p.mass_out[at + to[u]] = mass[from[u]];
+        if (l8 == 1) p.pos_out[at + to[u]] = pos[from[u]];
+      }
   }
 }
 

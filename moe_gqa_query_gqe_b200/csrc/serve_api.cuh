@@ -11,10 +11,7 @@
 
 namespace {
 
-#ifndef GQE_TU
-#define GQE_TU 0
-#endif
-constexpr int kTreeUmmaRows = GQE_TU;
+constexpr int kTreeUmmaRows = 32;
 int check_opt(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p != nullptr && !aligned16(p)) return GQE_ERR_INVALID_ARG;
@@ -88,11 +85,9 @@ int evict_list(const gqe_dims* d) { return d->T / 2 + 1; }
 size_t evict_ws_bytes(const gqe_dims* d, EvictParams* p, uint8_t* ws) {
   Carver c{ws};
   const size_t bg = (size_t)d->B * d->G;
-  int32_t* moves = c.take<int32_t>(bg);
   int32_t* holes = c.take<int32_t>(bg * evict_list(d));
   int32_t* late = c.take<int32_t>(bg * evict_list(d));
   if (p) {
-    p->moves = moves;
     p->holes = holes;
     p->late = late;
   }
@@ -307,11 +302,14 @@ int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink, int32_t recen
   p.sink = sink;
   p.recent = recent;
   p.list = evict_list(d);
+  // as many blocks a (sequence, group), up to a portable cluster, as two an SM
+  // allow; each holds its keys where they are no more than 96 KB
   const long long bg = (long long)d->B * d->G;
-  GQE_TRY(launch_pdl(evict_select_kernel, dim3((unsigned)bg), dim3(kEvictThreads), 0, st, p));
-  const long long most = std::max<long long>(1, std::min<long long>(keep, d->T / 2 + 1));
-  const long long blocks = std::min<long long>(cdiv(most, kMoveThreads / 8), std::max<long long>(1, cdiv(148 * 8, bg)));
-  return launch_pdl(evict_move_kernel, dim3((unsigned)blocks, (unsigned)bg), dim3(kMoveThreads), 0, st, p);
+  p.ncta = 1;
+  while (p.ncta < 8 && bg * p.ncta * 2 <= 2 * kTreeSms) p.ncta *= 2;
+  p.held = std::min((int)cdiv(cdiv(d->T, p.ncta), kEvictThreads) * kEvictThreads, 24576);
+  GQE_TRY(set_smem(cache_evict_kernel, p.held * 4));
+  return launch_pdl_cluster(cache_evict_kernel, dim3((unsigned)(bg * p.ncta)), dim3(kEvictThreads), p.held * 4, p.ncta, st, p);
 }
 
 }  // extern "C"

@@ -317,6 +317,79 @@ __device__ __forceinline__ bool tu_block(const TuTile& T, int col0, int valid, c
   return true;
 }
 
+// A tile's blocks of a unit, for one thread: everything that the loop needs of
+// the unit is here, and the function is not inlined, so that what the kernel
+// keeps besides does not push the scores out of the registers (inlined, the
+// loop spilled 290 bytes a thread).
+struct TuUnit {
+  TuTile T;
+  uint64_t *s_full, *mask_full, *v_full;
+  uint8_t* v_row;       // this thread's row of V's first stage
+  const uint4* mask;    // its token's ancestors
+  const uint32_t* bad;  // the word of s_bad with its V row
+  uint32_t mask_parity;
+  int first, nj, stride;  // blocks first, first + stride, ... below nj
+  int jdraft, left;       // the drafts' block; cached positions from the range's first block on
+  int n, row, col0;
+  bool warp_on;
+  uint32_t kv, cnt;  // blocks before the unit: of the range, of the tile
+  float m, l;
+};
+template <int D>
+__device__ __noinline__ bool tu_unit(TuUnit& u) {
+  const TuTile T = u.T;
+  float m_run = -INFINITY, l_run = 0.f;
+  uint32_t cnt = u.cnt;
+  const int first = u.first, nj = u.nj, stride = u.stride;
+  bool ok = true;
+  for (int jj = first; jj < nj; jj += stride, ++cnt) {
+    const bool drafts = jj == u.jdraft;
+    const int valid = drafts ? u.n : min(kTuBlock, u.left - jj * kTuBlock);
+    bool w_ok = !drafts || mbar_wait(u.mask_full, u.mask_parity, T.abort_flag);
+    if (w_ok && (valid < kTuBlock || drafts)) {
+      // this thread's value row: zeroed past the last valid one; without the
+      // values that are not finite in a drafted row
+      const uint32_t kvj = u.kv + jj;
+      w_ok = mbar_wait(&u.v_full[kvj % kTuVStages], (kvj / kTuVStages) & 1, T.abort_flag);
+      uint8_t* vs = u.v_row + (kvj % kTuVStages) * 16384;
+      if (w_ok && u.row >= valid) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vs + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+      } else if (w_ok && drafts && ((*u.bad >> (u.row & 31)) & 1u)) {
+        for (int c = 0; c < 32; ++c) {
+          uint32_t w = *reinterpret_cast<uint32_t*>(vs + 4 * c);
+          if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+          if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+          *reinterpret_cast<uint32_t*>(vs + 4 * c) = w;
+        }
+      }
+      fence_proxy_async_smem();
+    }
+    w_ok = w_ok && mbar_wait(u.s_full, cnt & 1, T.abort_flag);
+    if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
+    tc_fence_after();
+    if (!u.warp_on) {
+      // P of rows that are not stored may hold anything; the arrival must not
+      // fall into the block before, though
+      tc_fence_before();
+      mbar_arrive(T.s_free);
+      w_ok = jj == first || mbar_wait(T.pv_done, (cnt - 1) & 1, T.abort_flag);
+      if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
+      mbar_arrive(T.p_full);
+      continue;
+    }
+    if (drafts)
+      ok = tu_block<D, true>(T, u.col0, valid, *u.mask, jj == first, cnt, m_run, l_run);
+    else
+      ok = tu_block<D, false>(T, u.col0, valid, make_uint4(0u, 0u, 0u, 0u), jj == first, cnt, m_run, l_run);
+    if (!ok) break;
+  }
+  u.cnt = cnt;
+  u.m = m_run;
+  u.l = l_run;
+  return ok;
+}
+
 __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __grid_constant__ TreeUmmaParams P) {
   using S = TuSmem;
   const TreeParams& p = P.p;
@@ -633,58 +706,29 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
         }
         if (first < nj) mbar_arrive(&q_full[t]);
       }
-      float m_run = -INFINITY, l_run = 0.f;
-      for (int jj = first; jj < nj; jj += stride, ++cnt) {
-        const int j = it.j0 + jj;
-        const bool drafts = j == it.nblk - 1;
-        const int valid = drafts ? it.n : min(kTuBlock, it.L - j * kTuBlock);
-        bool w_ok = !drafts || mbar_wait(&mask_full[masks & 1], (masks >> 1) & 1, abort_flag);
-        if (w_ok && (valid < kTuBlock || drafts)) {
-          // this thread's value row: zeroed past the last valid one; without
-          // the values that are not finite in a drafted row
-          const uint32_t kvj = kv + jj;
-          w_ok = mbar_wait(&v_full[kvj % kTuVStages], (kvj / kTuVStages) & 1, abort_flag);
-          uint8_t* vs = smem + S::kV + (kvj % kTuVStages) * 16384 + row * 128;
-          if (w_ok && row >= valid) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vs + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
-          } else if (w_ok && drafts && ((s_bad[(masks & 1) * 4 + (row >> 5)] >> (row & 31)) & 1u)) {
-            for (int c = 0; c < 32; ++c) {
-              uint32_t w = *reinterpret_cast<uint32_t*>(vs + 4 * c);
-              if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-              if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-              *reinterpret_cast<uint32_t*>(vs + 4 * c) = w;
-            }
-          }
-          fence_proxy_async_smem();
-        }
-        w_ok = w_ok && mbar_wait(&s_full[t], cnt & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-        tc_fence_after();
-        if (!warp_on) {
-          // P of rows that are not stored may hold anything; the arrival must
-          // not fall into the block before, though
-          tc_fence_before();
-          mbar_arrive(&s_free[t]);
-          w_ok = jj == first || mbar_wait(&pv_done[t], (cnt - 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
-          mbar_arrive(&p_full[t]);
-          continue;
-        }
-        const int col0 = copy * width;
-        if (drafts) {
-          const uint4 mk = s_mask[(masks & 1) * kTreeMax + tok];
-          ok = D == 1   ? tu_block<1, true>(T, 0, valid, mk, jj == first, cnt, m_run, l_run)
-               : D == 2 ? tu_block<2, true>(T, col0, valid, mk, jj == first, cnt, m_run, l_run)
-                        : tu_block<4, true>(T, col0, valid, mk, jj == first, cnt, m_run, l_run);
-        } else {
-          const uint4 mk = make_uint4(0u, 0u, 0u, 0u);
-          ok = D == 1   ? tu_block<1, false>(T, 0, valid, mk, jj == first, cnt, m_run, l_run)
-               : D == 2 ? tu_block<2, false>(T, col0, valid, mk, jj == first, cnt, m_run, l_run)
-                        : tu_block<4, false>(T, col0, valid, mk, jj == first, cnt, m_run, l_run);
-        }
-        if (!ok) break;
-      }
+      TuUnit U;
+      U.T = T;
+      U.s_full = &s_full[t];
+      U.mask_full = &mask_full[masks & 1];
+      U.v_full = v_full;
+      U.v_row = smem + S::kV + row * 128;
+      U.mask = s_mask + (masks & 1) * kTreeMax + tok;
+      U.bad = s_bad + (masks & 1) * 4 + (row >> 5);
+      U.mask_parity = (masks >> 1) & 1;
+      U.first = first;
+      U.nj = nj;
+      U.stride = stride;
+      U.jdraft = it.nblk - 1 - it.j0;
+      U.left = it.L - it.j0 * kTuBlock;
+      U.n = it.n;
+      U.row = row;
+      U.col0 = copy * width;
+      U.warp_on = warp_on;
+      U.kv = kv;
+      U.cnt = cnt;
+      ok = D == 1 ? tu_unit<1>(U) : (D == 2 ? tu_unit<2>(U) : tu_unit<4>(U));
+      cnt = U.cnt;
+      const float m_run = U.m, l_run = U.l;
       if (!ok) break;
       const int mine = first < nj ? 1 : 0;  // has blocks
       // ---- the unit's end ------------------------------------------------------------
