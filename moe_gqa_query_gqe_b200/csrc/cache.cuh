@@ -104,13 +104,30 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t cluster_addr) {
   return v;
 }
 
+__device__ __forceinline__ int4 ld_dsmem_v4(uint32_t cluster_addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+// Every thread of the cluster, whether its warp has reconverged or not.
+__device__ __forceinline__ void cluster_sync_any() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // One cluster of `ncta` blocks per (sequence, group). Each block takes a
 // contiguous share of the rows, each warp a contiguous share of the block's, so
 // that (block, warp, step, lane) is the rows' order.
 //   1. Keys (mass and position, 8 bytes a row) are read once and held in shared
 //      memory, as far as they fit.
-//   2. The keep-th largest key by four 8-bit radix passes: a histogram per block,
-//      added over the cluster through distributed shared memory.
+//   2. The keep-th largest key by three radix passes of 11, 11 and 10 bits: a
+//      histogram per block, added over the cluster through distributed shared
+//      memory. (Masses lie within a few powers of two of one another: with 8
+//      bits the first pass counted into a handful of bins, and its atomics on
+//      them took half of the time.)
 //   3. A row stays if its key is larger, or equal and among the first of the
 //      equal ones; ranks by ballots, then sums over warps and blocks. The empty
 //      slots below keep and the staying rows past it go to two lists, in order.
@@ -120,13 +137,14 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t cluster_addr) {
 // leave, by the chain of the passes; the blocks of a cluster shorten both.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictCopies = 4;  // of the histogram, against atomics on one address
+constexpr int kEvictBins = 2048;
+constexpr int kEvictBinsEach = kEvictBins / kEvictThreads;  // of a thread
 struct EvictShared {
-  int hist[kEvictCopies][256];
-  int total[256];              // this block's histogram: read by the cluster
-  int counts[3];               // equal keys, holes, late rows of this block: read by the cluster
+  int hist[kEvictBins];
+  int total[2][kEvictBins];  // this block's histogram, of two passes in turn: read by the cluster
+  int counts[3];             // equal keys, holes, late rows of this block: read by the cluster
   int warp[3][kEvictWarps];
-  int pick[2];
+  int pick[3];
 };
 __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t s_keys[];
@@ -166,90 +184,100 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
   const int steps = min(len, max(0, n - base));  // rows of this warp
   uint32_t prefix = 0;
   int need = p.keep;  // rows still to be found among those that share the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < kEvictCopies * 256; i += kEvictThreads) sh.hist[i >> 8][i & 255] = 0;
+  int same = 0;       // how many share it
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const uint32_t digits = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
     __syncthreads();
-    int* hist = sh.hist[warp % kEvictCopies];
     for (int i0 = 0; i0 < steps; i0 += 128) {
       uint32_t key[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int i = i0 + u * 32 + lane;
         if (i < steps)
-          key[u] = shift == 24 ? evict_key(mass[base + i], pos[base + i], p.sink, recent_from) : key_at(i);
+          key[u] = pass == 0 ? evict_key(mass[base + i], pos[base + i], p.sink, recent_from) : key_at(i);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int i = i0 + u * 32 + lane;
         if (i >= steps) continue;
-        if (shift == 24 && held) mine[i] = key[u];
-        if (shift == 24 || (key[u] >> (shift + 8)) == prefix) atomicAdd(&hist[(key[u] >> shift) & 255u], 1);
+        if (pass == 0 && held) mine[i] = key[u];
+        if (pass == 0 || (key[u] >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&sh.hist[(key[u] >> shift) & digits], 1);
       }
     }
     __syncthreads();
-    if (tid < 256) {
-      int v = 0;
+    int* total = sh.total[pass & 1];
+    for (int i = tid; i < kEvictBins; i += kEvictThreads) total[i] = sh.hist[i];
+    cluster_sync_any();
+    // the highest bins first: thread t holds bins 2047 - 4 t downwards; sums over
+    // the threads before it. The cluster's eight histograms are loaded together: a
+    // load from another block takes a few hundred cycles.
+    static_assert(kEvictBinsEach == 4, "one 16-byte load a block");
+    const uint32_t mine4 = smem_u32(&total[kEvictBins - 4 - tid * 4]);
+    int4 part[8];
 #pragma unroll
-      for (int c = 0; c < kEvictCopies; ++c) v += sh.hist[c][tid];
-      sh.total[tid] = v;
+    for (int c = 0; c < 8; ++c)
+      if (c < p.ncta) part[c] = ld_dsmem_v4(mapa_shared(mine4, c));
+    int bins[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < p.ncta) {
+        bins[0] += part[c].w;
+        bins[1] += part[c].z;
+        bins[2] += part[c].y;
+        bins[3] += part[c].x;
+      }
+    const int sum = bins[0] + bins[1] + bins[2] + bins[3];
+    int above = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, above, d);
+      if (lane >= d) above += o;
     }
-    cluster_sync();
-    if (tid < 256) {
-      int v = 0;
-      for (int c = 0; c < p.ncta; ++c) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.total[tid]), c));
-      sh.hist[0][tid] = v;
+    if (lane == 31) sh.warp[0][warp] = above;
+    __syncthreads();
+    above -= sum;
+    for (int w = 0; w < warp; ++w) above += sh.warp[0][w];
+#pragma unroll
+    for (int i = 0; i < kEvictBinsEach; ++i) {
+      if (above < need && above + bins[i] >= need) {
+        sh.pick[0] = kEvictBins - 1 - tid * kEvictBinsEach - i;
+        sh.pick[1] = need - above;
+        sh.pick[2] = bins[i];
+      }
+      above += bins[i];
     }
     __syncthreads();
-    if (warp == 0) {
-      // lane l holds bins 8l .. 8l+7; sums from the top
-      int bins[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += bins[i] = sh.hist[0][lane * 8 + i];
-      int above = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_down_sync(0xffffffffu, above, d);
-        if (lane + d < 32) above += o;
-      }
-      above -= sum;  // in the lanes above this one
-      for (int i = 7; i >= 0; --i) {
-        if (above < need && above + bins[i] >= need) {
-          sh.pick[0] = lane * 8 + i;
-          sh.pick[1] = need - above;
-        }
-        above += bins[i];
-      }
-    }
-    cluster_sync();  // pick is there; every block has read the others' totals
-    prefix = (prefix << 8) | (uint32_t)sh.pick[0];
+    prefix = (prefix << (pass == 2 ? 10 : 11)) | (uint32_t)sh.pick[0];
     need = sh.pick[1];
+    same = sh.pick[2];
   }
-  // this warp's count of something, summed: over the warps before it and, for the
-  // cluster, over the block (slot `what` of counts)
+  // A count of each warp (warp[what]) and each block (counts[what]): the sum over
+  // what comes before this warp, in the block and in the cluster's blocks before.
   const uint32_t below = (1u << lane) - 1u;
-  auto before = [&](int what) {  // of the cluster's blocks before this one, and this block's warps before this warp
-    int v = 0;
-    for (int w = 0; w < warp; ++w) v += sh.warp[what][w];
-    for (int c = 0; c < rank; ++c) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[what]), c));
-    return v;
+  auto before = [&](int what) {
+    int v = lane < warp ? sh.warp[what][lane] : 0;
+    if (lane < rank) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[what]), lane));
+    return __reduce_add_sync(0xffffffffu, v);
   };
-  auto sum_warps = [&](int what) {
-    if (tid == 0) {
-      int v = 0;
-      for (int w = 0; w < kEvictWarps; ++w) v += sh.warp[what][w];
-      sh.counts[what] = v;
+  auto sum_warps = [&](int what) {  // (warp 0)
+    const int v = __reduce_add_sync(0xffffffffu, lane < kEvictWarps ? sh.warp[what][lane] : 0);
+    if (lane == 0) sh.counts[what] = v;
+  };
+  int eq = 0, eq0 = 0;
+  if (need < same) {  // only some of the equal keys' rows stay: their ranks
+    __syncthreads();
+    for (int i0 = 0; i0 < steps; i0 += 32) {
+      const int i = i0 + lane;
+      eq += __popc(__ballot_sync(0xffffffffu, i < steps && key_at(i) == prefix));
     }
-  };
-  int eq = 0;
-  for (int i0 = 0; i0 < steps; i0 += 32) {
-    const int i = i0 + lane;
-    eq += __popc(__ballot_sync(0xffffffffu, i < steps && key_at(i) == prefix));
+    if (lane == 0) sh.warp[0][warp] = eq;
+    __syncthreads();
+    if (warp == 0) sum_warps(0);
+    cluster_sync_any();
+    eq0 = before(0);
   }
-  if (lane == 0) sh.warp[0][warp] = eq;
-  __syncthreads();
-  sum_warps(0);
-  cluster_sync();
-  const int eq0 = before(0);
   int holes = 0, late = 0;
   eq = eq0;
   for (int i0 = 0; i0 < steps; i0 += 32) {
@@ -266,36 +294,63 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     sh.warp[2][warp] = late;
   }
   __syncthreads();
-  sum_warps(1);
-  __syncwarp();
-  sum_warps(2);
-  cluster_sync();
+  if (warp == 0) {
+    sum_warps(1);
+    sum_warps(2);
+  }
+  cluster_sync_any();
   holes = before(1);
   late = before(2);
   int32_t* hole_list = p.holes + (size_t)bg * p.list;
   int32_t* late_list = p.late + (size_t)bg * p.list;
   eq = eq0;
-  for (int i0 = 0; i0 < steps; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < steps ? key_at(i) : 0u;
-    const uint32_t e = __ballot_sync(0xffffffffu, i < steps && key == prefix);
-    const bool stays = i < steps && (key > prefix || (key == prefix && eq + __popc(e & below) < need));
-    eq += __popc(e);
-    const bool hole = i < steps && base + i < p.keep && !stays, past = base + i >= p.keep && stays;
-    const uint32_t hb = __ballot_sync(0xffffffffu, hole), lb = __ballot_sync(0xffffffffu, past);
-    if (hole) hole_list[holes + __popc(hb & below)] = base + i;
-    if (past) late_list[late + __popc(lb & below)] = base + i;
-    if (stays && !past) {
-      p.mass_out[at + base + i] = mass[base + i];
-      p.pos_out[at + base + i] = pos[base + i];
+  const bool copies = p.mass_out != p.mass_in || p.pos_out != p.pos_in;
+  for (int i0 = 0; i0 < steps; i0 += 128) {
+    float m[4];
+    int ps[4];
+    bool keeps[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * 32 + lane;
+      const uint32_t key = i < steps ? key_at(i) : 0u;
+      const uint32_t e = __ballot_sync(0xffffffffu, i < steps && key == prefix);
+      const bool stays = i < steps && (key > prefix || (key == prefix && eq + __popc(e & below) < need));
+      eq += __popc(e);
+      const bool hole = i < steps && base + i < p.keep && !stays, past = base + i >= p.keep && stays;
+      const uint32_t hb = __ballot_sync(0xffffffffu, hole), lb = __ballot_sync(0xffffffffu, past);
+      // (as many rows stay as the passes counted unless the masses change
+      // meanwhile: nothing is then written or moved out of range)
+      const int to = holes + __popc(hb & below), from = late + __popc(lb & below);
+      if (hole && to < p.list) hole_list[to] = base + i;
+      if (past && from < p.list) late_list[from] = base + i;
+      holes += __popc(hb);
+      late += __popc(lb);
+      keeps[u] = copies && stays && !past;
+      if (keeps[u]) {
+        m[u] = mass[base + i];
+        ps[u] = pos[base + i];
+      }
     }
-    holes += __popc(hb);
-    late += __popc(lb);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (keeps[u]) {
+        p.mass_out[at + base + i0 + u * 32 + lane] = m[u];
+        p.pos_out[at + base + i0 + u * 32 + lane] = ps[u];
+      }
   }
-  int moves = 0;
-  for (int c = 0; c < p.ncta; ++c) moves += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[1]), c));
+  int moves = 0, others = 0;
+  if (lane < p.ncta) {
+    moves = ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[1]), lane));
+    others = ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[2]), lane));
+  }
+  moves = __reduce_add_sync(0xffffffffu, moves);
+  others = __reduce_add_sync(0xffffffffu, others);
+  if (moves != others || moves > p.list) {
+    flag_bounds_error();
+    moves = 0;
+  }
   __threadfence();
-  cluster_sync();  // the lists are there; no block's shared memory is read from here on
+  cluster_sync_any();  // the lists are there; no block's shared memory is read from here on
   const int l8 = lane & 7;
   for (int i0 = (rank * kEvictWarps + warp) * 16; i0 < moves; i0 += p.ncta * kEvictWarps * 16) {
     int to[4], from[4];

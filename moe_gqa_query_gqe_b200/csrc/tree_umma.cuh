@@ -802,6 +802,7 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
         float o[kTuPiece];
         if (it.pair) {
           if (!warp_on) break;
+          __syncwarp();  // (whole again after the rows' own branches)
           uint32_t a[kTuPiece];
           tmem_ld4(T.tm_o + c, a);
 #pragma unroll
