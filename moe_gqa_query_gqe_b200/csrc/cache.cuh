@@ -85,7 +85,8 @@ struct EvictParams {
   int32_t* pos_out;
   int32_t* new_len;
   int32_t *holes, *late;  // [B*G][list] slots left empty below keep, rows kept past it
-  int B, G, cap, keep, sink, recent, list;
+  uint32_t* bits;         // [B*G][words] a bit a row: it stays
+  int B, G, cap, keep, sink, recent, list, words;
   int ncta;  // blocks of a cluster
   int held;  // keys a block can hold in shared memory
 };
@@ -126,22 +127,26 @@ __device__ __forceinline__ void cluster_sync_any() {
 //   2. The keep-th largest key by three radix passes of 11, 11 and 10 bits: a
 //      histogram per block, added over the cluster through distributed shared
 //      memory. (Masses lie within a few powers of two of one another: with 8
-//      bits the first pass counted into a handful of bins, and its atomics on
-//      them took half of the time.)
+//      bits the first pass counted into a handful of bins.) The second pass
+//      leaves its candidates in a list, which the third goes over.
 //   3. A row stays if its key is larger, or equal and among the first of the
-//      equal ones; ranks by ballots, then sums over warps and blocks. The empty
-//      slots below keep and the staying rows past it go to two lists, in order.
+//      equal ones: a bit a row. The empty slots below keep and the staying rows
+//      past it go to two lists, in order: ranks from the bits' counts, over lanes,
+//      warps and blocks.
 //   4. Row j of the one list moves into slot j of the other, eight lanes a row,
 //      K and V, four rows of a lane in flight.
-// Bound by the moved rows' bytes (1 KB a row, read and written), or, where few
-// leave, by the chain of the passes; the blocks of a cluster shorten both.
+// Bound by the moved rows' bytes (1 KB a row, read and written, in pieces of 128
+// bytes), or, where few leave, by the instructions a row of the passes and the
+// chain of cluster barriers.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
-constexpr int kEvictBinsEach = kEvictBins / kEvictThreads;  // of a thread
+constexpr int kEvictCands = 2048;
 struct EvictShared {
   int hist[kEvictBins];
   int total[2][kEvictBins];  // this block's histogram, of two passes in turn: read by the cluster
+  uint32_t cand[kEvictCands];
+  int ncand;
   int counts[3];             // equal keys, holes, late rows of this block: read by the cluster
   int warp[3][kEvictWarps];
   int pick[3];
@@ -182,28 +187,61 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     return held ? mine[i] : evict_key(mass[base + i], pos[base + i], p.sink, recent_from);
   };
   const int steps = min(len, max(0, n - base));  // rows of this warp
+  const uint32_t below = (1u << lane) - 1u;
   uint32_t prefix = 0;
   int need = p.keep;  // rows still to be found among those that share the prefix
   int same = 0;       // how many share it
+  if (tid == 0) sh.ncand = 0;
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const uint32_t digits = pass == 2 ? 1023u : 2047u;
     for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < steps; i0 += 128) {
-      uint32_t key[4];
+    if (pass == 0) {
+      for (int i0 = 0; i0 < steps; i0 += 128) {
+        float m[4];
+        int ps[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * 32 + lane;
-        if (i < steps)
-          key[u] = pass == 0 ? evict_key(mass[base + i], pos[base + i], p.sink, recent_from) : key_at(i);
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * 32 + lane;
+          if (i < steps) {
+            m[u] = mass[base + i];
+            ps[u] = pos[base + i];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * 32 + lane;
+          if (i >= steps) continue;
+          const uint32_t key = evict_key(m[u], ps[u], p.sink, recent_from);
+          if (held) mine[i] = key;
+          if (base + i < p.keep) {  // (a slot that is left gets its row's at the end)
+            p.mass_out[at + base + i] = m[u];
+            p.pos_out[at + base + i] = ps[u];
+          }
+          atomicAdd(&sh.hist[key >> 21], 1);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * 32 + lane;
-        if (i >= steps) continue;
-        if (pass == 0 && held) mine[i] = key[u];
-        if (pass == 0 || (key[u] >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&sh.hist[(key[u] >> shift) & digits], 1);
+    } else if (pass == 1 || sh.ncand > kEvictCands) {
+      const int cut = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
+      const uint32_t digits = pass == 1 ? 2047u : 1023u;
+      for (int i0 = 0; i0 < steps; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < steps ? key_at(i) : 0u;
+        const bool in = i < steps && (key >> cut) == prefix;
+        if (in) atomicAdd(&sh.hist[(key >> shift) & digits], 1);
+        if (pass == 1) {
+          const uint32_t all = __ballot_sync(0xffffffffu, in);
+          if (all) {
+            int to = 0;
+            if (lane == 0) to = atomicAdd(&sh.ncand, __popc(all));
+            to = __shfl_sync(0xffffffffu, to, 0) + __popc(all & below);
+            if (in && to < kEvictCands) sh.cand[to] = key;
+          }
+        }
+      }
+    } else {
+      for (int i = tid; i < sh.ncand; i += kEvictThreads) {
+        const uint32_t key = sh.cand[i];
+        if ((key >> 10) == prefix) atomicAdd(&sh.hist[key & 1023u], 1);
       }
     }
     __syncthreads();
@@ -213,7 +251,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     // the highest bins first: thread t holds bins 2047 - 4 t downwards; sums over
     // the threads before it. The cluster's eight histograms are loaded together: a
     // load from another block takes a few hundred cycles.
-    static_assert(kEvictBinsEach == 4, "one 16-byte load a block");
+    static_assert(kEvictBins == 4 * kEvictThreads, "one 16-byte load a block");
     const uint32_t mine4 = smem_u32(&total[kEvictBins - 4 - tid * 4]);
     int4 part[8];
 #pragma unroll
@@ -237,12 +275,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     }
     if (lane == 31) sh.warp[0][warp] = above;
     __syncthreads();
-    above -= sum;
-    for (int w = 0; w < warp; ++w) above += sh.warp[0][w];
+    above += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[0][lane] : 0) - sum;
 #pragma unroll
-    for (int i = 0; i < kEvictBinsEach; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (above < need && above + bins[i] >= need) {
-        sh.pick[0] = kEvictBins - 1 - tid * kEvictBinsEach - i;
+        sh.pick[0] = kEvictBins - 1 - tid * 4 - i;
         sh.pick[1] = need - above;
         sh.pick[2] = bins[i];
       }
@@ -255,7 +292,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
   }
   // A count of each warp (warp[what]) and each block (counts[what]): the sum over
   // what comes before this warp, in the block and in the cluster's blocks before.
-  const uint32_t below = (1u << lane) - 1u;
   auto before = [&](int what) {
     int v = lane < warp ? sh.warp[what][lane] : 0;
     if (lane < rank) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[what]), lane));
@@ -265,29 +301,37 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     const int v = __reduce_add_sync(0xffffffffu, lane < kEvictWarps ? sh.warp[what][lane] : 0);
     if (lane == 0) sh.counts[what] = v;
   };
-  int eq = 0, eq0 = 0;
-  if (need < same) {  // only some of the equal keys' rows stay: their ranks
+  // bits of the rows that stay, and how many holes and late rows they make
+  uint32_t* bits = p.bits + (size_t)bg * p.words + base / 32;
+  int holes = 0, late = 0;
+  auto count = [&](int i0, uint32_t stay) {  // of rows base + i0 .. + 31
+    const int left = min(32, steps - i0), under = min(max(p.keep - (base + i0), 0), 32);
+    const uint32_t there = left == 32 ? 0xffffffffu : (1u << left) - 1u;
+    const uint32_t low = under == 32 ? 0xffffffffu : (1u << under) - 1u;
+    holes += __popc(~stay & there & low);
+    late += __popc(stay & ~low);
+    if (lane == 0) bits[i0 / 32] = stay;
+  };
+  if (need == same) {
+    for (int i0 = 0; i0 < steps; i0 += 32)
+      count(i0, __ballot_sync(0xffffffffu, i0 + lane < steps && key_at(i0 + lane) >= prefix));
+  } else {  // only the first of the equal keys' rows stay
+    int eq = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < steps; i0 += 32) {
-      const int i = i0 + lane;
-      eq += __popc(__ballot_sync(0xffffffffu, i < steps && key_at(i) == prefix));
-    }
+    for (int i0 = 0; i0 < steps; i0 += 32)
+      eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < steps && key_at(i0 + lane) == prefix));
     if (lane == 0) sh.warp[0][warp] = eq;
     __syncthreads();
     if (warp == 0) sum_warps(0);
     cluster_sync_any();
-    eq0 = before(0);
-  }
-  int holes = 0, late = 0;
-  eq = eq0;
-  for (int i0 = 0; i0 < steps; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < steps ? key_at(i) : 0u;
-    const uint32_t e = __ballot_sync(0xffffffffu, i < steps && key == prefix);
-    const bool stays = i < steps && (key > prefix || (key == prefix && eq + __popc(e & below) < need));
-    eq += __popc(e);
-    holes += __popc(__ballot_sync(0xffffffffu, i < steps && base + i < p.keep && !stays));
-    late += __popc(__ballot_sync(0xffffffffu, base + i >= p.keep && stays));
+    eq = before(0);
+    for (int i0 = 0; i0 < steps; i0 += 32) {
+      const bool in = i0 + lane < steps;
+      const uint32_t key = in ? key_at(i0 + lane) : 0u;
+      const uint32_t e = __ballot_sync(0xffffffffu, in && key == prefix);
+      count(i0, __ballot_sync(0xffffffffu, in && (key > prefix || (key == prefix && eq + __popc(e & below) < need))));
+      eq += __popc(e);
+    }
   }
   if (lane == 0) {
     sh.warp[1][warp] = holes;
@@ -303,40 +347,33 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
   late = before(2);
   int32_t* hole_list = p.holes + (size_t)bg * p.list;
   int32_t* late_list = p.late + (size_t)bg * p.list;
-  eq = eq0;
-  const bool copies = p.mass_out != p.mass_in || p.pos_out != p.pos_in;
-  for (int i0 = 0; i0 < steps; i0 += 128) {
-    float m[4];
-    int ps[4];
-    bool keeps[4];
+  __syncwarp();
+  for (int i0 = 0; i0 < steps; i0 += 1024) {  // a lane, 32 rows
+    const int r0 = i0 + lane * 32, left = min(32, steps - r0), under = min(max(p.keep - (base + r0), 0), 32);
+    uint32_t h = 0, l = 0;
+    if (left > 0) {
+      const uint32_t stay = bits[r0 / 32];
+      const uint32_t there = left == 32 ? 0xffffffffu : (1u << left) - 1u;
+      const uint32_t low = under == 32 ? 0xffffffffu : (1u << under) - 1u;
+      h = ~stay & there & low;
+      l = stay & ~low;
+    }
+    const int hc = __popc(h), lc = __popc(l);
+    int hs = hc, ls = lc;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * 32 + lane;
-      const uint32_t key = i < steps ? key_at(i) : 0u;
-      const uint32_t e = __ballot_sync(0xffffffffu, i < steps && key == prefix);
-      const bool stays = i < steps && (key > prefix || (key == prefix && eq + __popc(e & below) < need));
-      eq += __popc(e);
-      const bool hole = i < steps && base + i < p.keep && !stays, past = base + i >= p.keep && stays;
-      const uint32_t hb = __ballot_sync(0xffffffffu, hole), lb = __ballot_sync(0xffffffffu, past);
-      // (as many rows stay as the passes counted unless the masses change
-      // meanwhile: nothing is then written or moved out of range)
-      const int to = holes + __popc(hb & below), from = late + __popc(lb & below);
-      if (hole && to < p.list) hole_list[to] = base + i;
-      if (past && from < p.list) late_list[from] = base + i;
-      holes += __popc(hb);
-      late += __popc(lb);
-      keeps[u] = copies && stays && !past;
-      if (keeps[u]) {
-        m[u] = mass[base + i];
-        ps[u] = pos[base + i];
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, hs, d), y = __shfl_up_sync(0xffffffffu, ls, d);
+      if (lane >= d) {
+        hs += x;
+        ls += y;
       }
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (keeps[u]) {
-        p.mass_out[at + base + i0 + u * 32 + lane] = m[u];
-        p.pos_out[at + base + i0 + u * 32 + lane] = ps[u];
-      }
+    // (as many rows stay as the passes counted unless the masses change
+    // meanwhile: nothing is then written or moved out of range)
+    for (int to = holes + hs - hc; h && to < p.list; h &= h - 1) hole_list[to++] = base + r0 + __ffs(h) - 1;
+    for (int to = late + ls - lc; l && to < p.list; l &= l - 1) late_list[to++] = base + r0 + __ffs(l) - 1;
+    holes += __shfl_sync(0xffffffffu, hs, 31);
+    late += __shfl_sync(0xffffffffu, ls, 31);
   }
   int moves = 0, others = 0;
   if (lane < p.ncta) {

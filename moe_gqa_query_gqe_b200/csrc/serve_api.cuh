@@ -82,12 +82,16 @@ int check_tree_dims(const gqe_dims* d, int cap) {
 }
 
 int evict_list(const gqe_dims* d) { return d->T / 2 + 1; }
+// words of a bit a row; a cluster's shares are whole blocks of rows
+int evict_words(const gqe_dims* d) { return (int)cdiv(d->T, 32) + 8 * kEvictWarps; }
 size_t evict_ws_bytes(const gqe_dims* d, EvictParams* p, uint8_t* ws) {
   Carver c{ws};
   const size_t bg = (size_t)d->B * d->G;
   int32_t* holes = c.take<int32_t>(bg * evict_list(d));
   int32_t* late = c.take<int32_t>(bg * evict_list(d));
+  uint32_t* bits = c.take<uint32_t>(bg * evict_words(d));
   if (p) {
+    p->bits = bits;
     p->holes = holes;
     p->late = late;
   }
@@ -302,6 +306,7 @@ int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink, int32_t recen
   p.sink = sink;
   p.recent = recent;
   p.list = evict_list(d);
+  p.words = evict_words(d);
   // as many blocks a (sequence, group), up to a portable cluster, as two an SM
   // allow and as have 1024 rows each (a barrier of the cluster costs more than
   // the rows that another block would take: 8 sequences x 8 groups x 4100 rows
