@@ -105,18 +105,23 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t cluster_addr) {
   return v;
 }
 
-__device__ __forceinline__ int4 ld_dsmem_v4(uint32_t cluster_addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+__device__ __forceinline__ int2 ld_dsmem_v2(uint32_t cluster_addr) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0,%1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
                : "r"(cluster_addr)
                : "memory");
   return v;
 }
-// Every thread of the cluster, whether its warp has reconverged or not.
-__device__ __forceinline__ void cluster_sync_any() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+// Every thread of the cluster, whether its warp has reconverged or not; within
+// one block the block's own barrier (a third of the time).
+__device__ __forceinline__ void cluster_sync_any(int ncta) {
+  if (ncta == 1) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  }
 }
 
 // One cluster of `ncta` blocks per (sequence, group). Each block takes a
@@ -138,20 +143,20 @@ __device__ __forceinline__ void cluster_sync_any() {
 // Bound by the moved rows' bytes (1 KB a row, read and written, in pieces of 128
 // bytes), or, where few leave, by the instructions a row of the passes and the
 // chain of cluster barriers.
-constexpr int kEvictThreads = 512;
-constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictWarps = kEvictThreads / 32;  // 32: a lane holds a warp's count
 constexpr int kEvictBins = 2048;
-constexpr int kEvictCands = 2048;
+constexpr int kEvictCands = 128;  // of a warp
+constexpr int kEvictBatch = 8;    // rows of a lane that are loaded together
 struct EvictShared {
   int hist[kEvictBins];
   int total[2][kEvictBins];  // this block's histogram, of two passes in turn: read by the cluster
-  uint32_t cand[kEvictCands];
-  int ncand;
+  uint32_t cand[kEvictWarps][kEvictCands];
   int counts[3];             // equal keys, holes, late rows of this block: read by the cluster
   int warp[3][kEvictWarps];
   int pick[3];
 };
-__global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kEvictThreads, 1) cache_evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t s_keys[];
   __shared__ EvictShared sh;
   pdl_wait();
@@ -191,16 +196,16 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
   uint32_t prefix = 0;
   int need = p.keep;  // rows still to be found among those that share the prefix
   int same = 0;       // how many share it
-  if (tid == 0) sh.ncand = 0;
+  int ncand = 0;      // this warp's keys that share the first digit
   for (int pass = 0; pass < 3; ++pass) {
     for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
     __syncthreads();
     if (pass == 0) {
-      for (int i0 = 0; i0 < steps; i0 += 128) {
-        float m[4];
-        int ps[4];
+      for (int i0 = 0; i0 < steps; i0 += 32 * kEvictBatch) {
+        float m[kEvictBatch];
+        int ps[kEvictBatch];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kEvictBatch; ++u) {
           const int i = i0 + u * 32 + lane;
           if (i < steps) {
             m[u] = mass[base + i];
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
           }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kEvictBatch; ++u) {
           const int i = i0 + u * 32 + lane;
           if (i >= steps) continue;
           const uint32_t key = evict_key(m[u], ps[u], p.sink, recent_from);
@@ -220,53 +225,58 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
           atomicAdd(&sh.hist[key >> 21], 1);
         }
       }
-    } else if (pass == 1 || sh.ncand > kEvictCands) {
+    } else if (pass == 1 || ncand > kEvictCands) {
       const int cut = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0;
       const uint32_t digits = pass == 1 ? 2047u : 1023u;
-      for (int i0 = 0; i0 < steps; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < steps ? key_at(i) : 0u;
-        const bool in = i < steps && (key >> cut) == prefix;
-        if (in) atomicAdd(&sh.hist[(key >> shift) & digits], 1);
-        if (pass == 1) {
-          const uint32_t all = __ballot_sync(0xffffffffu, in);
-          if (all) {
-            int to = 0;
-            if (lane == 0) to = atomicAdd(&sh.ncand, __popc(all));
-            to = __shfl_sync(0xffffffffu, to, 0) + __popc(all & below);
-            if (in && to < kEvictCands) sh.cand[to] = key;
+      for (int i0 = 0; i0 < steps; i0 += 32 * kEvictBatch) {
+        uint32_t key[kEvictBatch];
+#pragma unroll
+        for (int u = 0; u < kEvictBatch; ++u) {
+          const int i = i0 + u * 32 + lane;
+          key[u] = i < steps ? key_at(i) : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kEvictBatch; ++u) {
+          const bool in = i0 + u * 32 + lane < steps && (key[u] >> cut) == prefix;
+          if (in) atomicAdd(&sh.hist[(key[u] >> shift) & digits], 1);
+          if (pass == 1) {
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            const int to = ncand + __popc(all & below);
+            if (in && to < kEvictCands) sh.cand[warp][to] = key[u];
+            ncand += __popc(all);
           }
         }
       }
     } else {
-      for (int i = tid; i < sh.ncand; i += kEvictThreads) {
-        const uint32_t key = sh.cand[i];
+      __syncwarp();
+      for (int i = lane; i < ncand; i += 32) {
+        const uint32_t key = sh.cand[warp][i];
         if ((key >> 10) == prefix) atomicAdd(&sh.hist[key & 1023u], 1);
       }
     }
     __syncthreads();
     int* total = sh.total[pass & 1];
     for (int i = tid; i < kEvictBins; i += kEvictThreads) total[i] = sh.hist[i];
-    cluster_sync_any();
-    // the highest bins first: thread t holds bins 2047 - 4 t downwards; sums over
-    // the threads before it. The cluster's eight histograms are loaded together: a
-    // load from another block takes a few hundred cycles.
-    static_assert(kEvictBins == 4 * kEvictThreads, "one 16-byte load a block");
-    const uint32_t mine4 = smem_u32(&total[kEvictBins - 4 - tid * 4]);
-    int4 part[8];
+    cluster_sync_any(p.ncta);
+    // the highest bins first: thread t holds bins 2047 - 2 t and below; sums over
+    // the threads before it. The cluster's histograms are loaded together: a load
+    // from another block takes a thousand cycles here.
+    static_assert(kEvictBins == 2 * kEvictThreads, "one 8-byte load a block");
+    const int* mine2 = &total[kEvictBins - 2 - tid * 2];
+    int bins[2] = {mine2[1], mine2[0]};
+    if (p.ncta > 1) {
+      int2 part[7];
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c < p.ncta) part[c] = ld_dsmem_v4(mapa_shared(mine4, c));
-    int bins[4] = {0, 0, 0, 0};
+      for (int c = 1; c < 8; ++c)
+        if (c < p.ncta) part[c - 1] = ld_dsmem_v2(mapa_shared(smem_u32(mine2), (rank + c) & (p.ncta - 1)));
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c < p.ncta) {
-        bins[0] += part[c].w;
-        bins[1] += part[c].z;
-        bins[2] += part[c].y;
-        bins[3] += part[c].x;
-      }
-    const int sum = bins[0] + bins[1] + bins[2] + bins[3];
+      for (int c = 1; c < 8; ++c)
+        if (c < p.ncta) {
+          bins[0] += part[c - 1].y;
+          bins[1] += part[c - 1].x;
+        }
+    }
+    const int sum = bins[0] + bins[1];
     int above = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -277,9 +287,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     __syncthreads();
     above += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[0][lane] : 0) - sum;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if (above < need && above + bins[i] >= need) {
-        sh.pick[0] = kEvictBins - 1 - tid * 4 - i;
+        sh.pick[0] = kEvictBins - 1 - tid * 2 - i;
         sh.pick[1] = need - above;
         sh.pick[2] = bins[i];
       }
@@ -294,11 +304,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
   // what comes before this warp, in the block and in the cluster's blocks before.
   auto before = [&](int what) {
     int v = lane < warp ? sh.warp[what][lane] : 0;
-    if (lane < rank) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[what]), lane));
+    if (p.ncta > 1 && lane < rank) v += ld_dsmem_s32(mapa_shared(smem_u32(&sh.counts[what]), lane));
     return __reduce_add_sync(0xffffffffu, v);
   };
   auto sum_warps = [&](int what) {  // (warp 0)
-    const int v = __reduce_add_sync(0xffffffffu, lane < kEvictWarps ? sh.warp[what][lane] : 0);
+    const int v = __reduce_add_sync(0xffffffffu, sh.warp[what][lane]);
     if (lane == 0) sh.counts[what] = v;
   };
   // bits of the rows that stay, and how many holes and late rows they make
@@ -313,17 +323,32 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     if (lane == 0) bits[i0 / 32] = stay;
   };
   if (need == same) {
-    for (int i0 = 0; i0 < steps; i0 += 32)
-      count(i0, __ballot_sync(0xffffffffu, i0 + lane < steps && key_at(i0 + lane) >= prefix));
+    for (int i0 = 0; i0 < steps; i0 += 32 * kEvictBatch) {
+      uint32_t key[kEvictBatch];
+#pragma unroll
+      for (int u = 0; u < kEvictBatch; ++u) {
+        const int i = i0 + u * 32 + lane;
+        key[u] = i < steps ? key_at(i) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < kEvictBatch; ++u) {
+        const int i = i0 + u * 32;
+        if (i < steps) count(i, __ballot_sync(0xffffffffu, i + lane < steps && key[u] >= prefix));
+      }
+    }
   } else {  // only the first of the equal keys' rows stay
     int eq = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < steps; i0 += 32)
-      eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < steps && key_at(i0 + lane) == prefix));
+    if (ncand <= kEvictCands) {
+      for (int i = lane; i < ncand; i += 32) eq += sh.cand[warp][i] == prefix;
+    } else {
+      for (int i = lane; i < steps; i += 32) eq += key_at(i) == prefix;
+    }
+    eq = __reduce_add_sync(0xffffffffu, eq);
     if (lane == 0) sh.warp[0][warp] = eq;
     __syncthreads();
     if (warp == 0) sum_warps(0);
-    cluster_sync_any();
+    cluster_sync_any(p.ncta);
     eq = before(0);
     for (int i0 = 0; i0 < steps; i0 += 32) {
       const bool in = i0 + lane < steps;
@@ -342,7 +367,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     sum_warps(1);
     sum_warps(2);
   }
-  cluster_sync_any();
+  cluster_sync_any(p.ncta);
   holes = before(1);
   late = before(2);
   int32_t* hole_list = p.holes + (size_t)bg * p.list;
@@ -387,7 +412,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) cache_evict_kernel(const Evi
     moves = 0;
   }
   __threadfence();
-  cluster_sync_any();  // the lists are there; no block's shared memory is read from here on
+  cluster_sync_any(p.ncta);  // the lists are there; no block's shared memory is read from here on
   const int l8 = lane & 7;
   for (int i0 = (rank * kEvictWarps + warp) * 16; i0 < moves; i0 += p.ncta * kEvictWarps * 16) {
     int to[4], from[4];

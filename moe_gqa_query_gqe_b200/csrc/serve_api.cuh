@@ -307,14 +307,14 @@ int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink, int32_t recen
   p.recent = recent;
   p.list = evict_list(d);
   p.words = evict_words(d);
-  // as many blocks a (sequence, group), up to a portable cluster, as two an SM
-  // allow and as have 1024 rows each (a barrier of the cluster costs more than
-  // the rows that another block would take: 8 sequences x 8 groups x 4100 rows
-  // CLUSTER_FIGURES); each holds its keys where they are no more than 80 KB
+  // as many blocks a (sequence, group), up to a portable cluster, as there are SMs
+  // for and as have 4096 rows each (8 sequences x 8 groups x 4100 rows: 12.4 us with one
+  // block each, 20.6 with two of half as many threads); each holds its keys where
+  // they are no more than 160 KB
   const long long bg = (long long)d->B * d->G;
   p.ncta = 1;
-  while (p.ncta < 8 && bg * p.ncta * 2 <= 2 * kTreeSms && d->T >= 2048 * p.ncta) p.ncta *= 2;
-  p.held = std::min((int)cdiv(cdiv(d->T, p.ncta), kEvictThreads) * kEvictThreads, 20480);
+  while (p.ncta < 8 && bg * p.ncta * 2 <= kTreeSms && d->T >= 8192 * p.ncta) p.ncta *= 2;
+  p.held = std::min((int)cdiv(cdiv(d->T, p.ncta), kEvictThreads) * kEvictThreads, 40960);
   GQE_TRY(set_smem(cache_evict_kernel, p.held * 4));
   return launch_pdl_cluster(cache_evict_kernel, dim3((unsigned)(bg * p.ncta)), dim3(kEvictThreads), p.held * 4, p.ncta, st, p);
 }
