@@ -68,7 +68,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // bf16 tensor, 128-byte swizzle; dims/strides innermost first; strides in bytes
 // for dims 1..rank-1.
 int make_tmap(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-              const uint32_t* box) {
+              const uint32_t* box, CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   auto fn = encode_fn();
   if (!fn) return GQE_ERR_CUDA;
   cuuint64_t gd[5], gs[4];
@@ -80,7 +80,7 @@ int make_tmap(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
   }
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides[i];
   CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), gd, gs, bx, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GQE_OK : GQE_ERR_CUDA;
 }
@@ -94,11 +94,12 @@ int tmap_rows(CUtensorMap* tm, const void* base, long long rows, long long cols,
 }
 
 // [N, H, 64] bf16; box (64, bh, bn)
-int tmap_heads(CUtensorMap* tm, const void* base, long long N, int H, int bh, int bn) {
+int tmap_heads(CUtensorMap* tm, const void* base, long long N, int H, int bh, int bn,
+               CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   const uint64_t dims[3] = {64, (uint64_t)H, (uint64_t)N};
   const uint64_t strides[2] = {128, (uint64_t)H * 128};
   const uint32_t box[3] = {64, (uint32_t)bh, (uint32_t)bn};
-  return make_tmap(tm, base, 3, dims, strides, box);
+  return make_tmap(tm, base, 3, dims, strides, box, promotion);
 }
 
 // ---------------------------------------------------------------------------

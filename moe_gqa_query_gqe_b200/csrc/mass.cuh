@@ -50,7 +50,8 @@ struct MassParams {
 struct MassSmem {
   static constexpr int kLse = 0;                                // [1152] lse, log2 units
   static constexpr int kTok = kLse + kMassMaxRows * 4;          // [1152] place of the row's token in the path
-  static constexpr int kPrefix = kTok + kMassMaxRows * 2;       // [B + 1]
+  static constexpr int kOld = kTok + kMassMaxRows * 2;          // [4][256] sums so far
+  static constexpr int kPrefix = kOld + 4096;                   // [B + 1]
   static constexpr int kBar = kPrefix + (kTreeMaxB + 1) * 8;
   static constexpr int kQ = (kBar + 512 + 1023) / 1024 * 1024;  // chunks of 16 KB, then the ring's stages of 16 KB
 };
@@ -95,6 +96,37 @@ struct MassCursor {
   }
 };
 
+// A position's weights from N query rows, added to eight sums. `place` >= 0: the
+// position is the accepted token at that place, seen from there on.
+template <int N>
+__device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* lse, const int16_t* tok, float sl2, int place,
+                                         float (&sum)[8]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 l4 = reinterpret_cast<const float4*>(lse)[i];
+    float x[4], y[4];
+    ffma2(x[0], x[1], __uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]), sl2, sl2, -l4.x, -l4.y);
+    ffma2(x[2], x[3], __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]), sl2, sl2, -l4.z, -l4.w);
+    if (place >= 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (place > tok[4 * i + e]) x[e] = -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if ((2 * i + e) % kMassPolyEvery == kMassPolyEvery - 1) {
+        exp2_poly4(y[2 * e], y[2 * e + 1], x[2 * e], x[2 * e + 1]);
+      } else {
+        y[2 * e] = ex2_approx(x[2 * e]);
+        y[2 * e + 1] = ex2_approx(x[2 * e + 1]);
+      }
+    }
+    const int s = (4 * i) & 7;
+    fadd2(sum[s], sum[s + 1], sum[s], sum[s + 1], y[0], y[1]);
+    fadd2(sum[s + 2], sum[s + 3], sum[s + 2], sum[s + 3], y[2], y[3]);
+  }
+}
+
 __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __grid_constant__ MassParams P) {
   using S = MassSmem;
   const CommitParams& p = P.c;
@@ -111,6 +143,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_nan = reinterpret_cast<int*>(tmem_slot + 2);              // [2] units: a row's lse is NaN
   float* s_lse = reinterpret_cast<float*>(smem + S::kLse);
+  float* s_old = reinterpret_cast<float*>(smem + S::kOld);
   int16_t* s_tok = reinterpret_cast<int16_t*>(smem + S::kTok);
   long long* prefix = reinterpret_cast<long long*>(smem + S::kPrefix);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -285,12 +318,28 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
       const float nan = s_nan[units & 1] ? __int_as_float(0x7fffffff) : 0.f;
       if (wtid == 0) s_nan[(units + 1) & 1] = 0;
       const size_t at = ((size_t)it.b * p.G + it.g) * p.cap;
+      // a position's sum so far comes into shared memory three of the tile's blocks
+      // ahead, each thread its own (in registers the move from one block's to the
+      // next's waited for the load: 1200 of 2200 cycles a block)
+      auto fetch_old = [&](int jj, uint32_t slot) {
+        const int j = it.j0 + jj;
+        const bool in = jj < nj && j < it.nblk - 1 && j * kTuBlock + row < it.L;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(&s_old[(slot & 3) * 256 + wtid])),
+                     "l"(p.mass_in + at + (in ? j * kTuBlock + row : 0)), "r"(in ? 4 : 0)
+                     : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      uint32_t slot = 0;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) fetch_old((int)((kv & 1) ^ t) + 2 * i, i);
       for (int jj = (kv & 1) ^ t; jj < nj; jj += 2) {
         const int j = it.j0 + jj;
         const bool fresh = j == it.nblk - 1;  // the accepted rows
         const int s0 = fresh ? it.L : j * kTuBlock, valid = fresh ? it.n : min(kTuBlock, it.L - s0);
-        float old = 0.f;
-        if (!fresh && row < valid) old = p.mass_in[at + s0 + row];
+        fetch_old(jj + 6, slot + 3);
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+        const float old = s_old[(slot & 3) * 256 + wtid];
+        ++slot;
         float sum[8] = {nan, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int r0 = 0; r0 < it.R; r0 += 128, ++s_cnt) {
           const int buf = s_cnt & 1;
@@ -299,36 +348,16 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
           tc_fence_after();
           const int cols = min(128, Rp - r0);
           if (q * 32 < valid) {
-            for (int c0 = 0; c0 < cols; c0 += 16) {
+            int c0 = 0;
+            for (; c0 + 64 <= cols; c0 += 64) {
+              uint32_t a[64];
+              tmem_ld64(tm + buf * 256 + c0, a);
+              mass_add<64>(a, s_lse + r0 + c0, s_tok + r0 + c0, p.scale_log2, fresh ? row : -1, sum);
+            }
+            for (; c0 < cols; c0 += 16) {
               uint32_t a[16];
               tmem_ld16(tm + buf * 256 + c0, a);
-              const float4* ls = reinterpret_cast<const float4*>(s_lse + r0 + c0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 l4 = ls[i];
-                float x[4];
-                ffma2(x[0], x[1], __uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]), p.scale_log2, p.scale_log2, -l4.x,
-                      -l4.y);
-                ffma2(x[2], x[3], __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]), p.scale_log2, p.scale_log2,
-                      -l4.z, -l4.w);
-                if (fresh) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (row > s_tok[r0 + c0 + 4 * i + e]) x[e] = -INFINITY;
-                }
-                float y[4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  if ((2 * i + e) % kMassPolyEvery == kMassPolyEvery - 1) {
-                    exp2_poly4(y[2 * e], y[2 * e + 1], x[2 * e], x[2 * e + 1]);
-                  } else {
-                    y[2 * e] = ex2_approx(x[2 * e]);
-                    y[2 * e + 1] = ex2_approx(x[2 * e + 1]);
-                  }
-                }
-                fadd2(sum[(4 * i) & 7], sum[(4 * i + 1) & 7], sum[(4 * i) & 7], sum[(4 * i + 1) & 7], y[0], y[1]);
-                fadd2(sum[(4 * i + 2) & 7], sum[(4 * i + 3) & 7], sum[(4 * i + 2) & 7], sum[(4 * i + 3) & 7], y[2], y[3]);
-              }
+              mass_add<16>(a, s_lse + r0 + c0, s_tok + r0 + c0, p.scale_log2, fresh ? row : -1, sum);
             }
           }
           tc_fence_before();
@@ -339,6 +368,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
           p.mass_out[at + s0 + row] =
               old + (((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7])));
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (!ok) break;
       mbar_arrive(q_free);
       ++units;

@@ -18,6 +18,13 @@ int check_opt(std::initializer_list<const void*> ps) {
   return GQE_OK;
 }
 
+// [rows, G, 64] bf16 in boxes of one group's row at 128 positions. Rows of 128
+// bytes are all that a box touches of a position's G: fetching 256 bytes into L2
+// for each would read the neighbour's too.
+int tmap_group(CUtensorMap* tm, const void* base, long long rows, int G) {
+  return tmap_heads(tm, base, rows, G, 1, kTuBlock, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+}
+
 // The tree attention's kernel, its units and its grid. The tensor-core kernel
 // (tree_umma.cuh) takes more than kTreeUmmaRows rows a group, the other one
 // (tree.cuh) fewer. Neither the grid nor the workspace depends on the cache's
@@ -201,10 +208,10 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
   const dim3 grid((unsigned)t.blocks);
   if (t.umma) {
-    GQE_TRY(tmap_heads(&P.tmK, K_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
-    GQE_TRY(tmap_heads(&P.tmV, V_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
-    GQE_TRY(tmap_heads(&P.tmKn, K_new, (long long)d->B * d->T, d->G, 1, kTuBlock));
-    GQE_TRY(tmap_heads(&P.tmVn, V_new, (long long)d->B * d->T, d->G, 1, kTuBlock));
+    GQE_TRY(tmap_group(&P.tmK, K_cache, (long long)d->B * cap, d->G));
+    GQE_TRY(tmap_group(&P.tmV, V_cache, (long long)d->B * cap, d->G));
+    GQE_TRY(tmap_group(&P.tmKn, K_new, (long long)d->B * d->T, d->G));
+    GQE_TRY(tmap_group(&P.tmVn, V_new, (long long)d->B * d->T, d->G));
     GQE_TRY(set_smem(tree_attn_umma_kernel, TuSmem::kBytes));
     GQE_TRY(launch_pdl(tree_attn_umma_kernel, grid, dim3(kTuThreads), TuSmem::kBytes, st, P));
   } else {
@@ -265,7 +272,7 @@ int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path, const i
   MassParams P;
   memset(&P, 0, sizeof(P));
   P.c = p;
-  GQE_TRY(tmap_heads(&P.tmK, K_cache, (long long)d->B * cap, d->G, 1, kTuBlock));
+  GQE_TRY(tmap_group(&P.tmK, K_cache, (long long)d->B * cap, d->G));
   const int rows = d->T * (d->k + 1);
   P.nchunk = (int)cdiv(rows, 128);
   P.nstage = kMassMaxStages;
