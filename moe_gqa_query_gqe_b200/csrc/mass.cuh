@@ -48,7 +48,7 @@ struct MassParams {
   int step;         // G: the groups side by side; 1: ranges over all groups
 };
 struct MassSmem {
-  static constexpr int kLse = 0;                                // [1152] lse, log2 units
+  static constexpr int kLse = 0;                                // [1152] -lse, log2 units
   static constexpr int kTok = kLse + kMassMaxRows * 4;          // [1152] place of the row's token in the path
   static constexpr int kOld = kTok + kMassMaxRows * 2;          // [4][256] sums so far
   static constexpr int kPrefix = kOld + 4096;                   // [B + 1]
@@ -96,18 +96,20 @@ struct MassCursor {
   }
 };
 
-// A position's weights from N query rows, added to eight sums. `place` >= 0: the
-// position is the accepted token at that place, seen from there on.
-template <int N>
-__device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* lse, const int16_t* tok, float sl2, int place,
+// A position's weights from N query rows, added to eight sums; nlse = -lse. With
+// kFresh the position is the accepted token at `place`, seen from there on. (As
+// a condition in one function the places' loads and comparisons were issued for
+// every position, 4 of 9.5 instructions a score.)
+template <int N, bool kFresh>
+__device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* nlse, const int16_t* tok, float sl2, int place,
                                          float (&sum)[8]) {
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
-    const float4 l4 = reinterpret_cast<const float4*>(lse)[i];
+    const float4 l4 = reinterpret_cast<const float4*>(nlse)[i];
     float x[4], y[4];
-    ffma2(x[0], x[1], __uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]), sl2, sl2, -l4.x, -l4.y);
-    ffma2(x[2], x[3], __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]), sl2, sl2, -l4.z, -l4.w);
-    if (place >= 0) {
+    ffma2(x[0], x[1], __uint_as_float(a[4 * i]), __uint_as_float(a[4 * i + 1]), sl2, sl2, l4.x, l4.y);
+    ffma2(x[2], x[3], __uint_as_float(a[4 * i + 2]), __uint_as_float(a[4 * i + 3]), sl2, sl2, l4.z, l4.w);
+    if constexpr (kFresh) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (place > tok[4 * i + e]) x[e] = -INFINITY;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_free + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_nan = reinterpret_cast<int*>(tmem_slot + 2);              // [2] units: a row's lse is NaN
-  float* s_lse = reinterpret_cast<float*>(smem + S::kLse);
+  float* s_nlse = reinterpret_cast<float*>(smem + S::kLse);
   float* s_old = reinterpret_cast<float*>(smem + S::kOld);
   int16_t* s_tok = reinterpret_cast<int16_t*>(smem + S::kTok);
   long long* prefix = reinterpret_cast<long long*>(smem + S::kPrefix);
@@ -302,9 +304,9 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
         }
         *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * 16384 + (r & 127) * 128 + ((ch ^ (r & 7)) << 4)) = v;
         if (ch == 0) {
-          const float ls = tok >= 0 ? p.lse[qrow] * 1.4426950408889634f : INFINITY;  // (no row: every weight is 0)
+          const float ls = tok >= 0 ? p.lse[qrow] * -1.4426950408889634f : -INFINITY;  // (no row: every weight is 0)
           if (ls != ls) s_nan[units & 1] = 1;  // (the polynomial would lose it)
-          s_lse[r] = ls;
+          s_nlse[r] = ls;
           s_tok[r] = (int16_t)max(j, 0);
         }
       }
@@ -349,15 +351,22 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
           const int cols = min(128, Rp - r0);
           if (q * 32 < valid) {
             int c0 = 0;
+            if (fresh) {
+              for (; c0 < cols; c0 += 16) {
+                uint32_t a[16];
+                tmem_ld16(tm + buf * 256 + c0, a);
+                mass_add<16, true>(a, s_nlse + r0 + c0, s_tok + r0 + c0, p.scale_log2, row, sum);
+              }
+            }
             for (; c0 + 64 <= cols; c0 += 64) {
               uint32_t a[64];
               tmem_ld64(tm + buf * 256 + c0, a);
-              mass_add<64>(a, s_lse + r0 + c0, s_tok + r0 + c0, p.scale_log2, fresh ? row : -1, sum);
+              mass_add<64, false>(a, s_nlse + r0 + c0, nullptr, p.scale_log2, 0, sum);
             }
             for (; c0 < cols; c0 += 16) {
               uint32_t a[16];
               tmem_ld16(tm + buf * 256 + c0, a);
-              mass_add<16>(a, s_lse + r0 + c0, s_tok + r0 + c0, p.scale_log2, fresh ? row : -1, sum);
+              mass_add<16, false>(a, s_nlse + r0 + c0, nullptr, p.scale_log2, 0, sum);
             }
           }
           tc_fence_before();
