@@ -17,11 +17,10 @@
 //   else                           A and B hold the same rows and take the
 //                                  range's blocks in turn.
 //                                  With 64 rows or fewer a tile holds them
-//                                  twice, with 32 or fewer four times: each
-//                                  copy takes its half or quarter of the block's
-//                                  keys (P is zero in the others), so that all
-//                                  four warps share the exponentials. Tiles and
-//                                  copies are added at the end.
+//                                  twice: each copy takes its half of the
+//                                  block's keys (P is zero in the other), so
+//                                  that all four warps share the exponentials.
+//                                  Tiles and copies are added at the end.
 // A pair block costs half again what a block of the second kind does (weights 3
 // and 2): it is bound by exponentials, the other by the cache's bytes.
 //
@@ -84,7 +83,7 @@ struct TuItem {
   bool pair;           // two row tiles
   int nblk, j0, j1;    // blocks of the unit; this range's
   int unit;
-  __device__ __forceinline__ int copies() const { return rows > 64 ? 1 : (rows > 32 ? 2 : 4); }
+  __device__ __forceinline__ int copies() const { return rows > 64 ? 1 : 2; }
   __device__ __forceinline__ int row_base(int t) const { return s * kTuRows + (pair ? t * 128 : 0); }
   __device__ __forceinline__ bool has_drafts() const { return j1 == nblk; }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nblk; }
@@ -210,82 +209,40 @@ struct TuTile {
   float sl2;
 };
 
-template <int D>
-__device__ __forceinline__ void tu_load_scores(uint32_t taddr, float (&s)[128 / D]) {
-  if constexpr (D == 1) {
-    tmem_ld128f(taddr, s);
-  } else {
-    uint32_t r[128 / D];
-    if constexpr (D == 2) tmem_ld64(taddr, r); else tmem_ld32(taddr, r);
+// Sixty-four columns of S in registers.
+template <bool kMasked>
+__device__ __forceinline__ void tu_scores(uint32_t taddr, uint32_t b0, uint32_t b1, float (&s)[64]) {
+  uint32_t r[64];
+  tmem_ld64(taddr, r);
 #pragma unroll
-    for (int i = 0; i < 128 / D; ++i) s[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 64; ++i) {
+    s[i] = __uint_as_float(r[i]);
+    if constexpr (kMasked)
+      if (!(((i < 32 ? b0 : b1) >> (i & 31)) & 1u)) s[i] = -INFINITY;
   }
 }
-template <int D>
-__device__ __forceinline__ void tu_store_p(uint32_t taddr, const uint32_t (&pk)[64 / D]) {
-  if constexpr (D == 1) {
-    tmem_st64(taddr, pk);
-  } else {
-#pragma unroll
-    for (int h = 0; h < 4 / D; ++h) {
-      uint32_t r[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) r[i] = pk[h * 16 + i];
-      tmem_st16(taddr + h * 16, r);
-    }
-  }
-}
-
-// One block of keys for a thread's row: its 128 / D scores (columns col0 on),
-// softmax, P. `valid` keys of the block are there; with kDrafts the row sees
-// those of `mk`. First: the unit's first block of this tile.
-template <int D, bool kDrafts>
-__device__ __forceinline__ bool tu_block(const TuTile& T, int col0, int valid, const uint4& mk, bool first, uint32_t cnt,
-                                         float& m_run, float& l_run) {
-  constexpr int N = 128 / D;
-  float s[N];
-  tu_load_scores<D>(T.tm_s + col0, s);
-  tc_fence_before();
-  mbar_arrive(T.s_free);  // S may be overwritten by the next block's QK^T now
-  if constexpr (kDrafts) {
-#pragma unroll
-    for (int w = 0; w < N / 32; ++w) {
-      const uint32_t bits = D == 1 ? mask_word(mk, w) : mask_word(mk, col0 / 32 + w);
-#pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (!((bits >> c) & 1u)) s[w * 32 + c] = -INFINITY;
-    }
-  } else if (valid < kTuBlock) {
-#pragma unroll
-    for (int c = 0; c < N; ++c)
-      if (col0 + c >= valid) s[c] = -INFINITY;
-  }
+__device__ __forceinline__ float tu_max(const float (&s)[64]) {
   float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-  for (int c = 4; c < N; c += 8) {
+  for (int c = 4; c < 64; c += 8) {
     m4[0] = fmax3_nan(m4[0], s[c], s[c + 1]);
     m4[1] = fmax3_nan(m4[1], s[c + 2], s[c + 3]);
-    if (c + 4 < N) {
+    if (c + 4 < 64) {
       m4[2] = fmax3_nan(m4[2], s[c + 4], s[c + 5]);
       m4[3] = fmax3_nan(m4[3], s[c + 6], s[c + 7]);
     }
   }
-  const float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[1]), m4[2], m4[3]);
-  const float m_new = fmaxf(m_run, mx * T.sl2);
-  const float m_use = (m_new > m_run + kRescaleThreshold) ? m_new : m_run;
-  const float mu = m_use == -INFINITY ? 0.f : m_use;  // (nothing seen yet)
-  const float alpha = ex2_approx(m_run - mu);
-  const bool rescale = !first && m_use != m_run;
-  m_run = m_use;
+  return fmax3_nan(fmax3_nan(m4[0], m4[1], m4[1]), m4[2], m4[3]);
+}
+// P of sixty-four columns, as bf16 pairs; their sum is returned.
+template <bool kPoly>
+__device__ __forceinline__ float tu_exp(const float (&s)[64], float sl2, float mu, uint32_t (&pk)[32]) {
   float sm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  uint32_t pk[N / 2];
 #pragma unroll
-  for (int pi = 0; pi < N / 2; ++pi) {
+  for (int pi = 0; pi < 32; ++pi) {
     float x0, x1, y0, y1;
-    ffma2(x0, x1, s[2 * pi], s[2 * pi + 1], T.sl2, T.sl2, -mu, -mu);
-    // (a masked place of the draft block must be exactly zero: MUFU only; with
-    // copies the exponentials bind nothing)
-    if (D == 1 && !kDrafts && (pi % kTuPolyEvery) == kTuPolyEvery - 1) {
+    ffma2(x0, x1, s[2 * pi], s[2 * pi + 1], sl2, sl2, -mu, -mu);
+    if (kPoly && (pi % kTuPolyEvery) == kTuPolyEvery - 1) {
       exp2_poly4(y0, y1, x0, x1);
     } else {
       y0 = ex2_approx(x0);
@@ -294,7 +251,54 @@ __device__ __forceinline__ bool tu_block(const TuTile& T, int col0, int valid, c
     fadd2(sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], sm[2 * (pi & 3)], sm[2 * (pi & 3) + 1], y0, y1);
     pk[pi] = pack_bf16x2(y0, y1);
   }
-  l_run = l_run * alpha + (((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7])));
+  return ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+}
+__device__ __forceinline__ void tu_store_p(uint32_t taddr, const uint32_t (&pk)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = pk[h * 16 + i];
+    tmem_st16(taddr + h * 16, r);
+  }
+}
+
+// One block of keys for a thread's row: its 128 / D scores (columns col0 on),
+// softmax, P. With kMasked the row sees the keys of `mk` only (a function of its
+// own: as a condition the comparisons were issued for every block). The scores
+// are taken sixty-four at a time, the first half twice: all 128 in registers
+// left the loop spilling 100 bytes a thread, which took a fifth of its time.
+// First: the unit's first block of this tile.
+template <int D, bool kMasked>
+__device__ __forceinline__ bool tu_block(const TuTile& T, int col0, const uint4& mk, bool first, uint32_t cnt,
+                                         float& m_run, float& l_run) {
+  // (a masked place must be exactly zero: MUFU only; with copies the
+  // exponentials bind nothing)
+  constexpr bool kPoly = D == 1 && !kMasked;
+  float s[64];
+  float mx = -INFINITY;
+  if constexpr (D == 1) {
+    tu_scores<kMasked>(T.tm_s, mk.x, mk.y, s);
+    mx = tu_max(s);
+  }
+  const bool low = D == 1 || col0 == 0;  // (D = 2: the copy's columns)
+  tu_scores<kMasked>(T.tm_s + (D == 1 ? 64 : col0), D == 1 || !low ? mk.z : mk.x, D == 1 || !low ? mk.w : mk.y, s);
+  if constexpr (D == 2) {
+    tc_fence_before();
+    mbar_arrive(T.s_free);  // S may be overwritten by the next block's QK^T now
+  }
+  {
+    const float m2 = tu_max(s);
+    mx = fmax3_nan(mx, m2, m2);
+  }
+  const float m_new = fmaxf(m_run, mx * T.sl2);
+  const float m_use = (m_new > m_run + kRescaleThreshold) ? m_new : m_run;
+  const float mu = m_use == -INFINITY ? 0.f : m_use;  // (nothing seen yet)
+  const float alpha = ex2_approx(m_run - mu);
+  const bool rescale = !first && m_use != m_run;
+  m_run = m_use;
+  uint32_t pk[32];
+  l_run = l_run * alpha + tu_exp<kPoly>(s, T.sl2, mu, pk);
   if (!(mx < INFINITY)) l_run = __int_as_float(0x7fffffff);  // a score that is NaN or +inf: the row is NaN
   if (!first) {
     const bool w_ok = mbar_wait(T.pv_done, (cnt - 1) & 1, T.abort_flag);
@@ -311,7 +315,14 @@ __device__ __forceinline__ bool tu_block(const TuTile& T, int col0, int valid, c
       }
     }
   }
-  tu_store_p<D>(T.tm_p + col0 / 2, pk);
+  tu_store_p(T.tm_p + (D == 1 ? 32 : col0 / 2), pk);
+  if constexpr (D == 1) {
+    tu_scores<kMasked>(T.tm_s, mk.x, mk.y, s);
+    tc_fence_before();
+    mbar_arrive(T.s_free);
+    l_run += tu_exp<kPoly>(s, T.sl2, mu, pk);
+    tu_store_p(T.tm_p, pk);
+  }
   tc_fence_before();
   mbar_arrive(T.p_full);
   return true;
@@ -336,7 +347,7 @@ struct TuUnit {
   float m, l;
 };
 template <int D>
-__device__ __noinline__ bool tu_unit(TuUnit& u) {
+__device__ __forceinline__ bool tu_unit(TuUnit& u) {
   const TuTile T = u.T;
   float m_run = -INFINITY, l_run = 0.f;
   uint32_t cnt = u.cnt;
@@ -378,10 +389,18 @@ __device__ __noinline__ bool tu_unit(TuUnit& u) {
       mbar_arrive(T.p_full);
       continue;
     }
-    if (drafts)
-      ok = tu_block<D, true>(T, u.col0, valid, *u.mask, jj == first, cnt, m_run, l_run);
-    else
-      ok = tu_block<D, false>(T, u.col0, valid, make_uint4(0u, 0u, 0u, 0u), jj == first, cnt, m_run, l_run);
+    if (drafts || valid < kTuBlock) {
+      uint4 mk;
+      if (drafts) {
+        mk = *u.mask;
+      } else {  // the first `valid` of the block
+        auto word = [&](int w) { return valid >= 32 * w + 32 ? 0xffffffffu : (valid <= 32 * w ? 0u : (1u << (valid - 32 * w)) - 1u); };
+        mk = make_uint4(word(0), word(1), word(2), word(3));
+      }
+      ok = tu_block<D, true>(T, u.col0, mk, jj == first, cnt, m_run, l_run);
+    } else {
+      ok = tu_block<D, false>(T, u.col0, make_uint4(0u, 0u, 0u, 0u), jj == first, cnt, m_run, l_run);
+    }
     if (!ok) break;
   }
   u.cnt = cnt;
@@ -726,7 +745,7 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       U.warp_on = warp_on;
       U.kv = kv;
       U.cnt = cnt;
-      ok = D == 1 ? tu_unit<1>(U) : (D == 2 ? tu_unit<2>(U) : tu_unit<4>(U));
+      ok = D == 1 ? tu_unit<1>(U) : tu_unit<2>(U);
       cnt = U.cnt;
       const float m_run = U.m, l_run = U.l;
       if (!ok) break;
