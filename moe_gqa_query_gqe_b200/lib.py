@@ -208,27 +208,25 @@ def gqa_dense_forward(dims, x, Wq, Wk, Wv, Wo_dense, y, ws, stream=None) -> None
 _BF, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _checked(fn: str, names: tuple, dtypes: tuple, tensors: tuple, sizes: tuple) -> list:
-    """Data pointers of the tensors, and the handle of the current stream."""
-    device = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+def _checked(fn: str, names: tuple, dtypes: tuple, tensors: tuple, sizes: tuple, stream) -> list:
+    """Data pointers of the tensors, then the handle of the stream (None: the
+    current one)."""
+    device = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
     out = []
-    for i, t in enumerate(tensors):
+    for t, dtype, size in zip(tensors, dtypes, sizes):
         if t is None:
             out.append(None)
             continue
-        if t.dtype is not dtypes[i] or t.numel() != sizes[i] or t.get_device() != device or device < 0 or not t.is_contiguous():
-            raise GqeError(fn, -1, f"{names[i]} must be a contiguous {dtypes[i]} tensor of {sizes[i]} elements on the current "
+        if t.dtype is not dtype or t.numel() != size or t.get_device() != device or device < 0 or not t.is_contiguous():
+            raise GqeError(fn, -1, f"{names[len(out)]} must be a contiguous {dtype} tensor of {size} elements on the current "
                                    f"device (cuda:{device}), got {tuple(t.shape)} {t.dtype} on {t.device}"
                                    f"{'' if t.is_contiguous() else ', not contiguous'}")
         out.append(t.data_ptr())
+    if stream is None:
+        out.append(torch._C._cuda_getCurrentRawStream(device) if device >= 0 else 0)  # without the stream's Python object
+    else:
+        out.append(_stream(stream))
     return out
-
-
-def _current(stream):
-    """_stream without the Python object of the current stream."""
-    if stream is None and torch.cuda.is_initialized():
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return 0 if stream is None else _stream(stream)
 
 
 def _bytes(ws) -> int:
@@ -259,8 +257,8 @@ def gqe_qk_rope(dims, Q, K, wq, wk, sel, inv_freq, positions, Qo, Ko, *, layout=
     nq, nk = N * (G * k + 1) * 64, N * G * 64
     p = _checked("gqe_qk_rope", _ROPE_NAMES, _ROPE_TYPES,
                  (Q, K, wq, wk, sel, inv_freq if rot else None, positions, Qo, Ko),
-                 (nq, nk, (G * d.M + 1) * 64, G * 64, N * G * k, rot // 2, N, nq, nk))
-    _call("gqe_qk_rope", ctypes.byref(d), layout, rot, eps, scale, *p, _current(stream))
+                 (nq, nk, (G * d.M + 1) * 64, G * 64, N * G * k, rot // 2, N, nq, nk), stream)
+    _call("gqe_qk_rope", ctypes.byref(d), layout, rot, eps, scale, *p)
 
 
 def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, trained_len=0, beta_fast=32.0, beta_slow=1.0,
@@ -316,8 +314,9 @@ def gqe_tree_attn(dims, cap, Q, K_new, V_new, K_cache, V_cache, cache_len, draft
     rows, kn, kc = N * (G * d.k + 1), N * G * 64, B * cap * G * 64
     p = _checked("gqe_tree_attn", _TREE_NAMES, _TREE_TYPES,
                  (Q, K_new, V_new, K_cache, V_cache, cache_len, draft_len, parent, O, lse, ws),
-                 (rows * 64, kn, kn, kc, kc, B, B, N, rows * 64, rows, _bytes(ws)))
-    _call("gqe_tree_attn", ctypes.byref(d), cap, *p, _bytes(ws), _current(stream))
+                 (rows * 64, kn, kn, kc, kc, B, B, N, rows * 64, rows, _bytes(ws)), stream)
+    stream = p.pop()
+    _call("gqe_tree_attn", ctypes.byref(d), cap, *p, _bytes(ws), stream)
 
 
 def gqe_tree_commit(dims, cap, path, n_acc, positions, Q, lse, K_new, V_new, cache_len, K_cache, V_cache, pos, mass_in,
@@ -331,8 +330,8 @@ def gqe_tree_commit(dims, cap, path, n_acc, positions, Q, lse, K_new, V_new, cac
     rows, kn, kc, m = N * (G * d.k + 1), N * G * 64, B * cap * G * 64, B * G * cap
     p = _checked("gqe_tree_commit", _COMMIT_NAMES, _COMMIT_TYPES,
                  (path, n_acc, positions, Q, lse, K_new, V_new, cache_len, K_cache, V_cache, pos, mass_in, mass_out, new_len),
-                 (N, B, N, rows * 64, rows, kn, kn, B, kc, kc, m, m, m, B))
-    _call("gqe_tree_commit", ctypes.byref(d), cap, *p, _current(stream))
+                 (N, B, N, rows * 64, rows, kn, kn, B, kc, kc, m, m, m, B), stream)
+    _call("gqe_tree_commit", ctypes.byref(d), cap, *p)
 
 
 def gqe_cache_evict(dims, keep, sink, recent, cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out,
@@ -345,8 +344,9 @@ def gqe_cache_evict(dims, keep, sink, recent, cache_len, next_pos, K_cache, V_ca
     B, m = d.B, d.B * d.G * d.T
     p = _checked("gqe_cache_evict", _EVICT_NAMES, _EVICT_TYPES,
                  (cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out, new_len, ws),
-                 (B, B, m * 64, m * 64, m, m, m, m, B, _bytes(ws)))
-    _call("gqe_cache_evict", ctypes.byref(d), keep, sink, recent, *p, _bytes(ws), _current(stream))
+                 (B, B, m * 64, m * 64, m, m, m, m, B, _bytes(ws)), stream)
+    stream = p.pop()
+    _call("gqe_cache_evict", ctypes.byref(d), keep, sink, recent, *p, _bytes(ws), stream)
 
 
 def gqe_check_error(stream=None) -> int:
