@@ -71,7 +71,8 @@ struct TuSmem {
   static constexpr int kUp = kMask + 2 * kTreeMax * 16;      // [128] pointers of the doubling
   static constexpr int kBad = kUp + kTreeMax * 4;            // [2][4] drafts with values that are not finite
   static constexpr int kML = kBad + 32;                      // [2][128] m, l of the tiles
-  static constexpr int kPrefix = kML + 2 * 128 * 8;          // [B + 1] weight before each sequence
+  static constexpr int kWarp = kML + 2 * 128 * 8;            // [8] TuWarp of the softmax warps
+  static constexpr int kPrefix = kWarp + 8 * 128;            // [B + 1] weight before each sequence
   static constexpr int kBar = kPrefix + (kTreeMaxB + 1) * 8;
   static constexpr int kBytes = kBar + 512 + 1024;
 };
@@ -80,7 +81,7 @@ struct TuItem {
   int b, g, s;         // sequence, group, unit of the group
   int L, n, R;         // cached positions, drafted tokens, rows of the group
   int rows;            // rows of the unit
-  bool pair;           // two row tiles
+  int pair;            // two row tiles
   int nblk, j0, j1;    // blocks of the unit; this range's
   int unit;
   __device__ __forceinline__ int copies() const { return rows > 64 ? 1 : 2; }
@@ -199,6 +200,23 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// A softmax warp's place in its range, in shared memory: in registers it pushed
+// the scores out of them.
+struct TuWarp {
+  TuCursor cur;
+  TuItem it;
+  int more;
+};
+static_assert(sizeof(TuWarp) <= 128, "its slot");
+__device__ __forceinline__ TuItem tu_item(const TuWarp* w) {  // read anew at every call
+  TuItem it;
+  const volatile int* src = reinterpret_cast<const volatile int*>(&w->it);
+  int* dst = reinterpret_cast<int*>(&it);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(TuItem) / 4); ++i) dst[i] = src[i];
+  return it;
 }
 
 // The barriers and tensor-memory addresses of one tile's softmax warps.
@@ -695,17 +713,23 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       ++meets;
       return __all_sync(0xffffffffu, w_ok);
     };
-    while (ok && cur.next(P, it)) {
+    TuWarp* place = reinterpret_cast<TuWarp*>(smem + S::kWarp + (warp - 4) * 128);
+    if (lane == 0) place->cur = cur;
+    while (ok) {
+      if (lane == 0) place->more = place->cur.next(P, place->it);
+      __syncwarp();
+      if (!*reinterpret_cast<volatile int*>(&place->more)) break;
+      TuItem it = tu_item(place);
       const int nj = it.j1 - it.j0;
       const int stride = it.pair ? 1 : 2, first = it.pair ? 0 : (int)((kv & 1) ^ t);
       const int D = it.copies(), width = 128 / D;      // rows a copy has room for
       const int copy = row / width;
-      const int base = it.row_base(t), r = base + row % width;
-      const int nrow = min(width, it.R - base);        // rows of this tile
+      int base = it.row_base(t);
+      int nrow = min(width, it.R - base);              // rows of this tile
       const bool warp_on = q * 32 % width < nrow;
-      const int rc = min(r, it.R - 1);                 // (rows past the last repeat it and are not stored)
-      const int tok = tree_row_token(rc, it.n, p.k), slot = tree_row_slot(rc, it.n, it.g, p.k, p.G);
-      const size_t out = ((size_t)it.b * p.T + tok) * p.Ha + slot;
+      int rc = min(base + row % width, it.R - 1);      // (rows past the last repeat it and are not stored)
+      int tok = tree_row_token(rc, it.n, p.k), slot = tree_row_slot(rc, it.n, it.g, p.k, p.G);
+      size_t out = ((size_t)it.b * p.T + tok) * p.Ha + slot;
       {
         // this row of Q, swizzled as the MMA reads it. Every S of the unit
         // before has been read, so its Q is no longer in use.
@@ -749,6 +773,13 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       cnt = U.cnt;
       const float m_run = U.m, l_run = U.l;
       if (!ok) break;
+      it = tu_item(place);
+      base = it.row_base(t);
+      nrow = min(width, it.R - base);
+      rc = min(base + row % width, it.R - 1);
+      tok = tree_row_token(rc, it.n, p.k);
+      slot = tree_row_slot(rc, it.n, it.g, p.k, p.G);
+      out = ((size_t)it.b * p.T + tok) * p.Ha + slot;
       const int mine = first < nj ? 1 : 0;  // has blocks
       // ---- the unit's end ------------------------------------------------------------
       bool w_ok = mine == 0 || mbar_wait(&pv_done[t], (cnt - 1) & 1, abort_flag);
@@ -864,7 +895,7 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       }
       if (t == 0 && row == 0 && it.j0 == 0) {
         // the ranges that hold blocks of this unit
-        const long long ubase = cur.base - (long long)it.nblk * tu_weight(it.rows);
+        const long long ubase = place->cur.base - (long long)it.nblk * tu_weight(it.rows);
         p.unit_cta[it.unit] =
             make_int2(cta, tree_range_of(total, grid, ubase + (long long)(it.nblk - 1) * tu_weight(it.rows)) * step +
                                (step > 1 ? cta % step : 0));
@@ -876,7 +907,8 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
       }
       // the sums are read: the next unit's Q may take their place
       if (!it.pair && !(ok = meet())) break;
-      kv += nj;
+      kv += it.j1 - it.j0;
+      __syncwarp();
     }
   }
   __syncwarp();  // lanes that skipped a single-lane role wait for it
