@@ -365,6 +365,10 @@ int gqa_dense_forward(const gqe_dims* d, const void* x, const void* Wq,
  * that each row holds (a group's rows stay in any order once some were
  * evicted). Rows at and past cache_len[b] are never used, whatever they hold.
  *
+ * A workspace belongs to one call at a time: calls that may overlap (other
+ * streams, graphs replayed side by side) take one each. Nothing in it needs to
+ * be kept or zeroed between calls.
+ *
  * A length, index or expert out of range that only the device sees sets the
  * device check word (gqe_check_error returns GQE_ERR_DEVICE_CHECK) and the
  * sequence, or row, that it belongs to is skipped.
@@ -377,7 +381,8 @@ int gqa_dense_forward(const gqe_dims* d, const void* x, const void* Wq,
  *   (a, b) -> (a c - b s, b c + a s)               per pair i < rot/2
  *   c = scale * cos(pos * inv_freq[i]), s = scale * sin(pos * inv_freq[i])
  * Elements rot..63 are not rotated. Arithmetic in fp32, the result rounded
- * once; the angles are reduced in fp64, exact at any int32 position.
+ * once; the angles are reduced as 64-bit fractions of a turn, at any int32
+ * position.
  *
  * layout : enum gqe_rope_layout; rot even, 0..64 (0: the norms alone).
  * scale  : 1, or the attention factor of a frequency scaling that has one.

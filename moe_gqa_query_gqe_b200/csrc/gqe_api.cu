@@ -808,7 +808,7 @@ size_t gqe_workspace_bytes(const gqe_dims* d, int op) {
       c.take<__nv_bfloat16>(N * (size_t)variant_max_cols(d));              // variant A
       return c.off;
     }
-    case GQE_OP_TREE_ATTN: return d->T > kTreeMax ? 0 : tree_ws_bytes(d, nullptr, nullptr);
+    case GQE_OP_TREE_ATTN: return d->T > kTreeMax ? 0 : tree_ws_bytes(d);
     case GQE_OP_CACHE_EVICT: return evict_ws_bytes(d, nullptr, nullptr);
     default: return 0;
   }

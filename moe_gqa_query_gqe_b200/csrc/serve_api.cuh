@@ -11,7 +11,6 @@
 
 namespace {
 
-constexpr int kTreeUmmaRows = 32;
 int check_opt(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p != nullptr && !aligned16(p)) return GQE_ERR_INVALID_ARG;
@@ -25,30 +24,40 @@ int tmap_group(CUtensorMap* tm, const void* base, long long rows, int G) {
   return tmap_heads(tm, base, rows, G, 1, kTuBlock, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
-// The tree attention's kernel, its units and its grid. The tensor-core kernel
-// (tree_umma.cuh) takes more than kTreeUmmaRows rows a group, the other one
-// (tree.cuh) fewer. Neither the grid nor the workspace depends on the cache's
-// capacity.
+// The tree attention's kernel. Both cut the keys of all sequences into equal
+// ranges; the tensor-core kernel (tree_umma.cuh) has the higher rate and costs
+// some 12 us before its first block, the other one (tree.cuh) half of that. By
+// scores, the rows of a group times the positions that the caches can hold, with
+// 8 groups and one row a token (us, tree.cuh / tree_umma.cuh):
+//    32 rows   1 x 32000  27.2 / 23.5   4 x 32000  63.5 / 63.0   16 x 4000  46.2 / 48.7
+//    64 rows   1 x 16000  26.6 / 25.7   4 x 16000  58.7 / 58.5   16 x 2000  47.9 / 47.3
+//   128 rows   1 x 16000  36.9 / 42.1   4 x  8000  63.3 / 51.4   16 x 2000  68.7 / 59.3
+//   128 rows   4 x 32000 187.8 / 97.0
+bool tree_takes_umma(const gqe_dims* d, int cap) {
+  const long long R = (long long)d->T * d->k;
+  return R > 32 && R * d->G * d->B >= cdiv(20000000, cap);
+}
+
+// Units and grid of either kernel. Neither they nor the workspace depend on the
+// cache's capacity.
 struct TreePlan {
-  bool umma;
   int wr;          // row tiles of 16 a unit (tree.cuh)
   int urows, u0, u1, prow;
   int blocks, step;
   long long units;
 };
 constexpr int kTreeSms = 148;  // of a B200
-TreePlan tree_plan(const gqe_dims* d) {
+TreePlan tree_plan(const gqe_dims* d, bool umma) {
   TreePlan t;
   const int R = d->T * d->k, R0 = R + d->T;
-  t.umma = R > kTreeUmmaRows;
   t.wr = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
-  t.urows = t.umma ? kTuRows : 16 * t.wr;
+  t.urows = umma ? kTuRows : 16 * t.wr;
   t.u0 = (int)cdiv(R0, t.urows);
   t.u1 = (int)cdiv(R, t.urows);
   t.prow = std::min(t.urows, R0);
   const int per_seq = t.u0 + (d->G - 1) * t.u1;
   t.units = (long long)d->B * per_seq;
-  if (t.umma) {
+  if (umma) {
     // the groups side by side where every group is one tile; else ranges over
     // all units, whose weights differ
     t.step = R0 <= 128 ? d->G : 1;
@@ -60,8 +69,8 @@ TreePlan tree_plan(const gqe_dims* d) {
   }
   return t;
 }
-size_t tree_ws_bytes(const gqe_dims* d, TreeParams* p, uint8_t* ws) {
-  const TreePlan t = tree_plan(d);
+size_t tree_carve(const gqe_dims* d, bool umma, TreeParams* p, uint8_t* ws) {
+  const TreePlan t = tree_plan(d, umma);
   Carver c{ws};
   const size_t rows = (size_t)2 * t.blocks * t.prow;
   float* ml = c.take<float>(rows * 2);
@@ -78,6 +87,9 @@ size_t tree_ws_bytes(const gqe_dims* d, TreeParams* p, uint8_t* ws) {
     p->step = t.step;
   }
   return c.off;
+}
+size_t tree_ws_bytes(const gqe_dims* d) {
+  return std::max(tree_carve(d, false, nullptr, nullptr), tree_carve(d, true, nullptr, nullptr));
 }
 
 // Sequences, drafted tokens and capacity of the cache operators.
@@ -184,11 +196,12 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   GQE_TRY(check_ws(ws, ws_bytes, gqe_workspace_bytes(d, GQE_OP_TREE_ATTN)));
   GQE_TRY(check_device());
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const TreePlan t = tree_plan(d);
+  const bool umma = tree_takes_umma(d, cap);
+  const TreePlan t = tree_plan(d, umma);
   TreeUmmaParams P;
   memset(&P, 0, sizeof(P));
   TreeParams& p = P.p;
-  tree_ws_bytes(d, &p, static_cast<uint8_t*>(ws));
+  tree_carve(d, umma, &p, static_cast<uint8_t*>(ws));
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.Kn = static_cast<const __nv_bfloat16*>(K_new);
   p.Vn = static_cast<const __nv_bfloat16*>(V_new);
@@ -207,7 +220,7 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   p.cap = cap;
   p.scale_log2 = 1.4426950408889634f / sqrtf(64.f);
   const dim3 grid((unsigned)t.blocks);
-  if (t.umma) {
+  if (umma) {
     GQE_TRY(tmap_group(&P.tmK, K_cache, (long long)d->B * cap, d->G));
     GQE_TRY(tmap_group(&P.tmV, V_cache, (long long)d->B * cap, d->G));
     GQE_TRY(tmap_group(&P.tmKn, K_new, (long long)d->B * d->T, d->G));

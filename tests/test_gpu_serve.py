@@ -231,16 +231,79 @@ def test_tree_matches_oracle(d, cap, lens, drafts, shape):
     assert torch.equal(O2, O) and torch.equal(lse2, lse) and torch.equal(O3, O)
 
 
-@pytest.mark.parametrize("k,T", [(1, 12), (4, 40)])
-def test_tree_values_that_are_not_finite_reach_descendants_only(k, T):
+def roomier(x, cap):
+    """The same sequences in caches of `cap` rows, all the others NaN."""
+    x = dict(x)
+    for key in ("Kc", "Vc"):
+        c = torch.full((x[key].shape[0], cap, *x[key].shape[2:]), NAN, dtype=torch.bfloat16, device="cuda")
+        c[:, :x[key].shape[1]] = x[key].cuda()
+        x[key] = c
+    return x
+
+
+def large_capacity(d):
+    """A capacity that has the call take the kernel for long caches (20 million scores)."""
+    return 20_000_000 // (d.B * d.G * d.T * d.k) + 130
+
+
+@pytest.mark.parametrize("d,cap,lens,drafts,shape", [c for c in TREE if c[0].T * c[0].k > 32],
+                         ids=[f"b{c[0].B}t{c[0].T}g{c[0].G}k{c[0].k}_{c[4]}_{max(c[2])}" for c in TREE if c[0].T * c[0].k > 32])
+def test_tree_in_a_large_cache_matches_oracle(d, cap, lens, drafts, shape):
+    x = tree_inputs(d, cap, lens, drafts, shape, 12)
+    big = large_capacity(d)
+    v = cu(roomier(x, big))
+    O, lse = run_tree(d, big, v)
+    ok()
+    check_tree(d, x, O, lse)
+    O2, lse2 = run_tree(d, big, v)
+    O3, _ = run_tree(d, big, v, with_lse=False)
+    ok()
+    assert torch.equal(O2, O) and torch.equal(lse2, lse) and torch.equal(O3, O)
+
+
+@pytest.mark.parametrize("B,T,k,lens", [(3, 128, 2, [20000, 0, 7001]), (2, 70, 1, [30000, 12345]), (2, 34, 1, [40001, 128])])
+def test_tree_long_caches_match_the_formula(B, T, k, lens):
+    """Lengths at which a sequence's keys are cut into many ranges, against
+    torch in 64 bits (the oracle's loops would take minutes)."""
+    d = Dims(B=B, T=T, D=64, G=4, M=2, k=k)
+    x = tree_inputs(d, max(lens) + 3, lens, None, "chain", 13)
+    big = max(large_capacity(d), max(lens) + 3)
+    O, lse = run_tree(d, big, cu(roomier(x, big)))
+    ok()
+    Ha = d.G * k + 1
+    for b, L in enumerate(lens):
+        rows = slice(b * T, (b + 1) * T)
+        late = torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1)
+        for g in range(d.G):
+            K = torch.cat([x["Kc"][b, :L, g], x["Kn"][rows, g]]).cuda().double()
+            V = torch.cat([x["Vc"][b, :L, g], x["Vn"][rows, g]]).cuda().double()
+            for h in ref.group_slots(g, d.G, k):
+                q = x["Q"][rows, h].cuda().double()
+                s = q @ K.T / 8.0
+                s[:, L:][late] = -float("inf")
+                p = torch.softmax(s, 1)
+                size = (q.abs() @ K.abs().T).amax(1, keepdim=True) / 8.0 * 2.0 ** -17
+                terms = p @ V.abs()
+                want = p @ V
+                # besides the terms above: l adds up to 40 thousand terms in fp32, 2^-24 a step along chains of at most 64
+                # a thread and 2^10 blocks
+                tol = HALF * (want.abs() + terms) + (2 * size + 2.0 ** -13) * terms
+                within(O[rows, h], f64(want), f64(tol), f"O {b} {h}")
+                ls = torch.logsumexp(s, 1)
+                within(lse[rows, h], f64(ls), f64(size[:, 0]) + 2.0 ** -14 + 2.0 ** -20 * (1 + np.abs(f64(ls))), f"lse {b} {h}")
+
+
+@pytest.mark.parametrize("k,T,large", [(1, 12, False), (4, 40, False), (4, 40, True), (1, 50, True)])
+def test_tree_values_that_are_not_finite_reach_descendants_only(k, T, large):
     d = Dims(B=1, T=T, D=64, G=2, M=4, k=k)
     x = tree_inputs(d, 90, [70], None, "tree", 5)
+    cap = large_capacity(d) if large else 90
     par = x["parent"].numpy()
     sees = ref.ancestors(par, T)
     clean = {key: t.clone() if torch.is_tensor(t) else t for key, t in x.items()}
     x["Vn"][3, 1, 7], x["Vn"][6, 1, 8], x["Kn"][8, 0, 2] = float("inf"), NAN, NAN
-    O, lse = (f64(t) for t in run_tree(d, 90, cu(x)))
-    Oc, lsec = (f64(t) for t in run_tree(d, 90, cu(clean)))
+    O, lse = (f64(t) for t in run_tree(d, cap, cu(roomier(x, cap))))
+    Oc, lsec = (f64(t) for t in run_tree(d, cap, cu(roomier(clean, cap))))
     ok()
     hit = np.zeros(O.shape, bool)
     g1, g0 = slice(k, 2 * k), list(range(k)) + [2 * k]
@@ -256,13 +319,15 @@ def test_tree_values_that_are_not_finite_reach_descendants_only(k, T):
     assert np.isnan(lse[sees[:, 8]][:, g0]).all() and np.array_equal(lse[:, g1], lsec[:, g1])
 
 
-def test_tree_extreme_scores():
+@pytest.mark.parametrize("T", [4, 40])
+def test_tree_extreme_scores(T):
     """Scores of several thousand either way: the softmax is a choice of one key."""
-    d = Dims(B=1, T=4, D=64, G=4, M=2, k=1)
+    d = Dims(B=1, T=T, D=64, G=4, M=2, k=1)
     x = tree_inputs(d, 300, [280], None, "tree", 6)
     x["Q"] *= 64
     x["Kc"][:, 17] *= 32
-    O, lse = run_tree(d, 300, cu(x))
+    cap = 300 if T == 4 else large_capacity(d)
+    O, lse = run_tree(d, cap, cu(roomier(x, cap)))
     ok()
     check_tree(d, x, O, lse)
 
