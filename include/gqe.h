@@ -414,7 +414,7 @@ int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale,
  *      parent [B*T] int32: the parent of token i, parent < i, or -1 for a
  *      child of the cached sequence; NULL: a chain, parent[i] = i - 1. A
  *      parent that is neither is recorded and taken as -1.
- * Out: O [B*T, G*k+1, 64] bf16; lse [B*T, G*k+1] fp32, log sum_s exp(q.k_s / 8)
+ * Out: O [B*T, G*k+1, 64] bf16, not Q itself; lse [B*T, G*k+1] fp32, log sum_s exp(q.k_s / 8)
  *      over the attended rows, or NULL. Rows i >= draft_len[b] are left as they
  *      were.
  * What a masked row holds never reaches a result, infinities and NaN included.
@@ -450,7 +450,7 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q,
  *      pos [B, G, cap], or NULL: the same entries.
  * Out: mass_out [B, G, cap] fp32, entries below L + n; it may be mass_in.
  *      Both NULL: the weights are not accumulated, Q and lse are not read.
- *      new_len [B] = L + n; not cache_len itself.
+ *      new_len [B] = L + n; neither cache_len nor n_acc itself.
  * ws : none.
  */
 int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path,
@@ -475,8 +475,8 @@ int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path,
  *      next token; mass_in [B, G, T] fp32; pos_in [B, G, T] int32.
  * In/out: K_cache, V_cache [B, T, G, 64] bf16.
  * Out: mass_out, pos_out: the entries of the rows below new_len; they may be
- *      mass_in and pos_in. new_len [B] = min(cache_len, keep); not cache_len
- *      itself.
+ *      mass_in and pos_in. new_len [B] = min(cache_len, keep); neither
+ *      cache_len nor next_pos itself.
  * ws : gqe_workspace_bytes(d, GQE_OP_CACHE_EVICT).
  */
 int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink,

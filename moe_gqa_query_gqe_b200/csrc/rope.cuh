@@ -75,8 +75,7 @@ __device__ __forceinline__ void turn2(float& a0, float& a1, float& b0, float& b1
 }
 
 template <int kLayout, int kThreads>
-__global__ void __launch_bounds__(kThreads)
-    qk_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const RopeParams p) {
   __shared__ float4 s_cos[2][kRopeMaxTpb][8], s_sin[2][kRopeMaxTpb][8];
   extern __shared__ uint8_t rope_raw[];
   __shared__ unsigned long long s_turn[32];

@@ -193,6 +193,7 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q, const void* K_n
   GQE_TRY(check_tree_dims(d, cap));
   GQE_TRY(check_ptrs({Q, K_new, V_new, K_cache, V_cache, cache_len, O}));
   GQE_TRY(check_opt({draft_len, parent, lse}));
+  if (O == Q) return GQE_ERR_INVALID_ARG;
   GQE_TRY(check_ws(ws, ws_bytes, gqe_workspace_bytes(d, GQE_OP_TREE_ATTN)));
   GQE_TRY(check_device());
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -254,7 +255,7 @@ int gqe_tree_commit(const gqe_dims* d, int32_t cap, const int32_t* path, const i
   GQE_TRY(check_opt({path, n_acc, positions, Q, lse, pos, mass_in, mass_out}));
   if ((mass_in == nullptr) != (mass_out == nullptr)) return GQE_ERR_INVALID_ARG;
   if (mass_in != nullptr && (Q == nullptr || lse == nullptr)) return GQE_ERR_INVALID_ARG;
-  if (new_len == cache_len) return GQE_ERR_INVALID_ARG;
+  if (new_len == cache_len || new_len == n_acc) return GQE_ERR_INVALID_ARG;
   GQE_TRY(check_device());
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CommitParams p;
@@ -303,7 +304,7 @@ int gqe_cache_evict(const gqe_dims* d, int32_t keep, int32_t sink, int32_t recen
   GQE_TRY(check_dims(d));
   if (keep < 1 || sink < 0 || recent < 0 || (long long)sink + recent > keep) return GQE_ERR_INVALID_ARG;
   GQE_TRY(check_ptrs({cache_len, next_pos, K_cache, V_cache, mass_in, mass_out, pos_in, pos_out, new_len}));
-  if (new_len == cache_len) return GQE_ERR_INVALID_ARG;
+  if (new_len == cache_len || new_len == next_pos) return GQE_ERR_INVALID_ARG;
   GQE_TRY(check_ws(ws, ws_bytes, gqe_workspace_bytes(d, GQE_OP_CACHE_EVICT)));
   GQE_TRY(check_device());
   cudaStream_t st = static_cast<cudaStream_t>(stream);

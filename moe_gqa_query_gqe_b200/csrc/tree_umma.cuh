@@ -346,10 +346,7 @@ __device__ __forceinline__ bool tu_block(const TuTile& T, int col0, const uint4&
   return true;
 }
 
-// A tile's blocks of a unit, for one thread: everything that the loop needs of
-// the unit is here, and the function is not inlined, so that what the kernel
-// keeps besides does not push the scores out of the registers (inlined, the
-// loop spilled 290 bytes a thread).
+// A tile's blocks of a unit, for one thread: all that the loop needs of the unit.
 struct TuUnit {
   TuTile T;
   uint64_t *s_full, *mask_full, *v_full;

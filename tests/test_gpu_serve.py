@@ -510,6 +510,8 @@ EVICT = [
     (Dims(B=1, T=40000, D=64, G=1, M=8, k=1), [39999], 39998, 0, 0),
     (Dims(B=2, T=3000, D=64, G=8, M=2, k=1), [3000, 2999], 1500, 700, 800),
     (Dims(B=1, T=70001, D=64, G=2, M=4, k=1), [70001], 9000, 8, 1000),
+    # more rows than a cluster holds keys of
+    (Dims(B=1, T=400_000, D=64, G=1, M=8, k=1), [399_999], 100_000, 4, 1000),
 ]
 
 
@@ -583,6 +585,31 @@ def test_evict_length_out_of_range_is_reported():
         sub = {k: t[[0, 2]] for k, t in x.items()}
         check_evict(d.with_(B=2), 30, 1, 5, sub, [t[[0, 2]] for t in got])
     assert gqe.gqe_check_error() == 0
+
+
+def test_most_sequences():
+    """1024 sequences, as many as the dimensions allow, some without drafts or
+    cache, through tree attention, commit and eviction."""
+    d, cap = Dims(B=1024, T=2, D=64, G=8, M=1, k=1), 12
+    lens, drafts = [(7 * b) % 10 for b in range(1024)], [b % 3 for b in range(1024)]
+    x = tree_inputs(d, cap, lens, drafts, "chain", 17)
+    O, lse = run_tree(d, cap, cu(x))
+    ok()
+    check_tree(d, x, O, lse)
+    c = commit_inputs(d, cap, lens, drafts, "none", 18)
+    Kc, Vc, pos, mass, new_len = run_commit(d, cap, cu(c))
+    ok()
+    want = ref.tree_commit(None, drafts, c["positions"].numpy(), c["Q"], c["lse"], c["Kn"], c["Vn"], lens, c["Kc"], c["Vc"],
+                           c["pos"].numpy(), c["mass"], d.B, d.T, d.G, d.k)
+    np.testing.assert_array_equal(f64(Kc), want["K"])
+    np.testing.assert_array_equal(pos.cpu().numpy(), want["pos"])
+    np.testing.assert_array_equal(new_len.cpu().numpy(), want["len"])
+    used = np.broadcast_to(np.arange(cap)[None, None] < want["len"][:, None, None], want["mass"].shape)
+    rel = 2.0 ** -17 * want["score"] + 2.0 ** -20 * (1 + float(c["lse"].abs().max()) + want["score"]) + 2.0 ** -19
+    within(f64(mass)[used], want["mass"][used], rel * want["mass"][used] + 1e-12, "mass")
+    e = evict_inputs(d.with_(T=cap), lens, 19)
+    check_evict(d.with_(T=cap), 5, 1, 2, e, run_evict(d.with_(T=cap), 5, 1, 2, cu(e)))
+    ok()
 
 
 # ---- together ------------------------------------------------------------------------------

@@ -159,13 +159,13 @@ def test_tree_workspace():
     assert gqe.workspace_bytes(D.with_(k=3), gqe.OP_TREE_ATTN) == 0
 
 
-def _tree(d=D, cap=100, Q=P, Kn=P, Vn=P, Kc=P, Vc=P, L=P, n=None, par=None, O=P, lse=None, ws=P, nbytes=1 << 40):
+def _tree(d=D, cap=100, Q=P, Kn=P, Vn=P, Kc=P, Vc=P, L=P, n=None, par=None, O=2 * P, lse=None, ws=P, nbytes=1 << 40):
     return _raw("gqe_tree_attn", d, cap, Q, Kn, Vn, Kc, Vc, L, n, par, O, lse, ws, nbytes, None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(Q=None), -1), (dict(Kn=None), -1), (dict(Vn=None), -1), (dict(Kc=None), -1), (dict(Vc=None), -1), (dict(L=None), -1),
-    (dict(O=None), -1), (dict(O=P + 8), -1), (dict(lse=P + 4), -1), (dict(par=P + 4), -1), (dict(n=P + 4), -1), (dict(cap=0), -1),
+    (dict(O=None), -1), (dict(O=P), -1), (dict(O=P + 8), -1), (dict(lse=P + 4), -1), (dict(par=P + 4), -1), (dict(n=P + 4), -1), (dict(cap=0), -1),
     (dict(cap=-5), -1), (dict(d=D.with_(T=129)), -2), (dict(cap=1 << 30), -2), (dict(ws=None), -3), (dict(ws=P + 16), -3),
     (dict(nbytes=16), -3), (dict(d=D.with_(dh=32)), -2)])
 def test_tree_refusals(kw, code):
@@ -179,7 +179,7 @@ def _commit(d=D, cap=100, path=None, n=None, positions=None, Q=P, lse=P, Kn=P, V
 
 @pytest.mark.parametrize("kw,code", [
     (dict(Kn=None), -1), (dict(Vn=None), -1), (dict(L=None), -1), (dict(Kc=None), -1), (dict(Vc=None), -1), (dict(new=None), -1),
-    (dict(new=P), -1), (dict(mi=None), -1), (dict(mo=None), -1), (dict(Q=None), -1), (dict(lse=None), -1), (dict(path=P + 4), -1),
+    (dict(new=P), -1), (dict(n=2 * P), -1), (dict(mi=None), -1), (dict(mo=None), -1), (dict(Q=None), -1), (dict(lse=None), -1), (dict(path=P + 4), -1),
     (dict(pos=P + 4), -1), (dict(positions=P + 4), -1), (dict(n=P + 4), -1), (dict(cap=0), -1), (dict(d=D.with_(T=200)), -2)])
 def test_commit_refusals(kw, code):
     assert _commit(**kw) == code
@@ -192,7 +192,7 @@ def _evict(d=D, keep=8, sink=1, recent=2, L=P, nxt=P, Kc=P, Vc=P, mi=P, mo=P, pi
 @pytest.mark.parametrize("kw,code", [
     (dict(keep=0), -1), (dict(keep=-1), -1), (dict(sink=-1), -1), (dict(recent=-1), -1), (dict(sink=4, recent=5), -1),
     (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), -1), (dict(L=None), -1), (dict(nxt=None), -1), (dict(Kc=None), -1),
-    (dict(mo=None), -1), (dict(po=P + 4), -1), (dict(new=P), -1), (dict(ws=None), -3), (dict(nbytes=8), -3), (dict(ws=P + 64), -3)])
+    (dict(mo=None), -1), (dict(po=P + 4), -1), (dict(new=P), -1), (dict(nxt=2 * P), -1), (dict(ws=None), -3), (dict(nbytes=8), -3), (dict(ws=P + 64), -3)])
 def test_evict_refusals(kw, code):
     assert _evict(**kw) == code
 
