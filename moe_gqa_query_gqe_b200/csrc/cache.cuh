@@ -140,9 +140,11 @@ __device__ __forceinline__ void cluster_sync_any(int ncta) {
 //      warps and blocks.
 //   4. Row j of the one list moves into slot j of the other, eight lanes a row,
 //      K and V, four rows of a lane in flight.
-// Bound by the moved rows' bytes (1 KB a row, read and written, in pieces of 128
-// bytes), or, where few leave, by the instructions a row of the passes and the
-// chain of cluster barriers.
+// Bound by the moved rows' bytes (K and V, 256 bytes read and 256 written a row, in
+// pieces of 128), or, where few leave, by the instructions a row of the passes and
+// the chain of barriers. Measured, 8 sequences of 8 groups: 30000 to 32768 rows to
+// 4096 59 us, 25 of them before the first move (floor 21: 8 bytes a row and the
+// moves at the copy's rate); 4100 to 4096 12.3 us.
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;  // 32: a lane holds a warp's count
 constexpr int kEvictBins = 2048;

@@ -29,6 +29,11 @@
 // values of half go through shared memory. A thread keeps its head, so that
 // addresses advance by a constant; cosines and sines are computed once a chunk,
 // for the next one; products are packed in pairs (f32x2).
+//
+// Measured, Q and K of 8 groups: 1 x 131072 tokens of 25 heads 171-177 us =
+// 4.8-5.0 TB/s of 6.5 that a copy reaches (265 us with loads through registers
+// and each thread its own angles); 8 x 2048 of 17 heads 18.6 us, of which 8 are
+// the start and the end of a short kernel; one token 2.3 us.
 #pragma once
 
 #include "attn2.cuh"

@@ -32,6 +32,13 @@
 //   warps 4..11 softmax, one thread a row: Q into shared memory at the start of
 //               a unit; then per block S from TMEM, the running maximum
 //               (rescaled lazily) and sum, P as bf16 into TMEM
+// Bounds: one exponential a (row, position), 16 a clock and SM on the MUFU (one
+// pair in kTuPolyEvery on the FMA pipe), against 256 flops: 4 x 128 tokens of two
+// rows a group over 131072 positions of 8 groups take 253 us for the exponentials,
+// 179 for the products and 164 for the bytes. Measured there: 476-533 us, 549-614
+// TFLOP/s. The two softmax warps of a scheduler wait for their own chains (issue
+// slots 30-35% used, MUFU 54% of the time). Sixteen warps, a row over four
+// threads, took 821-855 us (96 registers a thread spill).
 // What a masked row holds is kept out in three places: masked scores are
 // replaced, not added to; value rows past the last valid one are zeroed before
 // P V; drafted values that are not finite are zeroed too, and added at the end
@@ -285,7 +292,8 @@ __device__ __forceinline__ void tu_store_p(uint32_t taddr, const uint32_t (&pk)[
 // softmax, P. With kMasked the row sees the keys of `mk` only (a function of its
 // own: as a condition the comparisons were issued for every block). The scores
 // are taken sixty-four at a time, the first half twice: all 128 in registers
-// left the loop spilling 100 bytes a thread, which took a fifth of its time.
+// spill 116 bytes a thread and take a sixth longer (4 x 128 tokens of two rows
+// a group over 131072 positions: 562 us against 478).
 // First: the unit's first block of this tile.
 template <int D, bool kMasked>
 __device__ __forceinline__ bool tu_block(const TuTile& T, int col0, const uint4& mk, bool first, uint32_t cnt,
