@@ -35,10 +35,13 @@
 // Bounds: one exponential a (row, position), 16 a clock and SM on the MUFU (one
 // pair in kTuPolyEvery on the FMA pipe), against 256 flops: 4 x 128 tokens of two
 // rows a group over 131072 positions of 8 groups take 253 us for the exponentials,
-// 179 for the products and 164 for the bytes. Measured there: 476-533 us, 549-614
-// TFLOP/s. The two softmax warps of a scheduler wait for their own chains (issue
-// slots 30-35% used, MUFU 54% of the time). Sixteen warps, a row over four
-// threads, took 821-855 us (96 registers a thread spill).
+// 179 for the products and 164 for the bytes. Measured there: 476 us (615
+// TFLOP/s) call after call on the same inputs, 529 over several sets in turn. The
+// two softmax warps of a scheduler wait for their own chains (issue slots 30-35%
+// used, MUFU 54% of the time). Sixteen warps, a row over four threads, took
+// 821-855 us (96 registers a thread spill); the next scores loaded from tensor
+// memory during a block's exponentials, in pieces of 32, 525 against 479 (88 bytes
+// a thread spill).
 // What a masked row holds is kept out in three places: masked scores are
 // replaced, not added to; value rows past the last valid one are zeroed before
 // P V; drafted values that are not finite are zeroed too, and added at the end
@@ -61,7 +64,9 @@ constexpr int kTuThreads = 384;
 constexpr int kTuRegsLow = 88, kTuRegsHigh = 208;  // 88*128 + 208*256 = 168*384
 constexpr int kTuBlock = 128;                      // keys of a block
 constexpr int kTuRows = 256;                       // rows of a unit
-constexpr int kTuPolyEvery = 8;  // every n-th pair of exponentials on the FMA pipe (as in attn2.cuh)
+// Every n-th pair of exponentials on the FMA pipe (4 x 128 tokens of two rows a
+// group over 131072 positions: 497 us with 16, 485 with 8 or 6, 476 with 4).
+constexpr int kTuPolyEvery = 4;
 
 struct TreeUmmaParams {
   CUtensorMap tmK, tmV;    // caches as [B*cap][G][64], box (64, 1, 128)
