@@ -75,7 +75,7 @@ struct MassCursor {
   __device__ __forceinline__ bool next(const CommitParams& p, MassItem& it) {
     while (b < p.B && base < x1) {
       commit_lens(p, b, it.L, it.n);
-      if (it.n < 0 || it.L + it.n == 0) {
+      if (it.n <= 0) {  // (nothing accepted: no weight, no unit in any role; mass_keep)
         ++b;
         g = only >= 0 ? only : 0;
         continue;
@@ -134,6 +134,44 @@ __device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* nl
   }
 }
 
+// Sequences that accept nothing keep their sums: where those go to another
+// buffer, all blocks of threads copy them, a piece of 1024 positions of one
+// (sequence, group) at a time, by the 256 threads that would add. Nothing of such
+// a sequence goes through the barriers: a unit without query rows would have its
+// summing threads wait for no product, and run phases ahead of the threads that
+// issue them.
+__device__ __forceinline__ void mass_keep(const CommitParams& p, const long long* prefix, int wtid) {
+  constexpr int kPiece = 1024;
+  const int lane = wtid & 31;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int L = 0, n = -1;
+    if (b < p.B && prefix[b + 1] == prefix[b]) commit_lens(p, b, L, n);
+    const int pieces = n == 0 ? (L + kPiece - 1) / kPiece : 0;  // of each group
+    int sum = pieces * p.G;                                     // below 2^31 over a warp: B * cap * G / 1024
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int total = __shfl_sync(0xffffffffu, sum, 31);
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+      const int at = __popc(__ballot_sync(0xffffffffu, sum <= i));  // the lane whose sequence it is
+      const int len = __shfl_sync(0xffffffffu, L, at), each = __shfl_sync(0xffffffffu, pieces, at);
+      const int r = i - (__shfl_sync(0xffffffffu, sum, at) - each * p.G);
+      const size_t row = ((size_t)(b0 + at) * p.G + r / each) * p.cap;
+      const int s = r % each * kPiece + wtid;
+      float v[kPiece / 256];
+#pragma unroll
+      for (int u = 0; u < kPiece / 256; ++u)
+        if (s + u * 256 < len) v[u] = p.mass_in[row + s + u * 256];
+#pragma unroll
+      for (int u = 0; u < kPiece / 256; ++u)
+        if (s + u * 256 < len) p.mass_out[row + s + u * 256] = v[u];
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __grid_constant__ MassParams P) {
   using S = MassSmem;
   const CommitParams& p = P.c;
@@ -181,7 +219,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
       int L, n;
       commit_lens(p, b, L, n);
       long long w = 0;
-      if (n >= 0 && L + n > 0) {
+      if (n > 0) {
         w = (L + kTuBlock - 1) / kTuBlock + 1;
         if (P.step == 1) w *= mass_weight(n * (p.k + 1)) + (long long)(p.G - 1) * mass_weight(n * p.k);
       }
@@ -388,6 +426,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
       ++units;
       kv += nj;
     }
+    if (ok && p.mass_out != p.mass_in) mass_keep(p, prefix, wtid);
   }
   __syncwarp();
   tc_fence_before();
