@@ -416,9 +416,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
           mbar_arrive(&s_free[t * 2 + buf]);
         }
         if (!ok) break;
-        if (row < valid)
-          p.mass_out[at + s0 + row] =
-              old + (((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+        if (row < valid) {
+          float w = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+          // a place whose path index is out of range holds no token (its key here is zero)
+          if (fresh && commit_token(p, it.b, row) < 0) w = 0.f;
+          p.mass_out[at + s0 + row] = old + w;
+        }
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (!ok) break;

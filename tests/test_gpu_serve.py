@@ -500,6 +500,35 @@ def test_commit_rows_out_of_range_are_reported():
     assert gqe.gqe_check_error() == 0
 
 
+@pytest.mark.parametrize("d,cap,lens,acc", [(Dims(B=3, T=5, D=64, G=4, M=2, k=1), 40, [10, 20, 30], [3, 4, 5]),
+                                            (Dims(B=2, T=60, D=64, G=2, M=8, k=4), 300, [200, 130], [60, 41])], ids=["few", "many"])
+def test_commit_path_index_out_of_range_adds_nothing(d, cap, lens, acc):
+    """Its place keeps its K, V and position with a sum of 0; its query rows add
+    nothing to the others' sums; new_len counts the place."""
+    x = commit_inputs(d, cap, lens, acc, "path", 4)
+    j, L, n = acc[1] - 2, lens[1], acc[1]
+    token = int(x["path"][1, j])
+    for bad in (-1, d.T, 2 ** 31 - 1):
+        v = cu(x)
+        v["path"][1, j] = bad
+        Kc, Vc, pos, mass, new_len = run_commit(d, cap, v)
+        assert gqe.gqe_check_error() == -7
+        assert new_len.tolist() == [a + b for a, b in zip(lens, acc)]
+        assert torch.equal(Kc[1, L + j], v["Kc"][1, L + j]) and torch.equal(Vc[1, L + j], v["Vc"][1, L + j])
+        assert torch.equal(pos[1, :, L + j], v["pos"][1, :, L + j]) and (mass[1, :, L + j] == 0).all()
+        # the formula without that token's rows: a log-sum of +infinity is a weight of zero
+        silent = x["lse"].clone()
+        silent[d.T + token] = float("inf")
+        want = ref.tree_commit(x["path"].numpy(), acc, x["positions"].numpy(), x["Q"], silent, x["Kn"], x["Vn"], lens, x["Kc"], x["Vc"],
+                               x["pos"].numpy(), x["mass"], d.B, d.T, d.G, d.k)
+        keep = np.arange(L + n) != L + j
+        np.testing.assert_array_equal(f64(Kc)[1, :L + n][keep], want["K"][1, :L + n][keep])
+        rel = 2.0 ** -17 * want["score"] + 2.0 ** -20 * (1 + float(x["lse"].abs().max()) + want["score"]) + d.T * (d.k + 1) * 2.0 ** -23
+        m = want["mass"][1, :, :L + n][:, keep]
+        within(f64(mass)[1, :, :L + n][:, keep], m, rel * m + 1e-12, "mass")
+    assert gqe.gqe_check_error() == 0
+
+
 # ---- eviction ------------------------------------------------------------------------------
 EVICT = [
     (Dims(B=1, T=8, D=64, G=8, M=1, k=1), [8], 7, 1, 1),
