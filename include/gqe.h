@@ -440,6 +440,8 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q,
  *      + sum over j with s <= L + j, and over the group's query rows (k, and
  *        the shared head's in group 0), of exp(q.k_s / 8 - lse)
  * for every s < L + n, which adds up to one for each query row.
+ * lse belongs to these queries and keys, so that no weight is above one (but for
+ * rounding); weights below 2^-126 add nothing.
  * A path index outside [0, T) is recorded: its token adds no weight, its row
  * L + j keeps what K_cache, V_cache and pos held, with a sum of 0, and new_len
  * counts it all the same (the rows behind it stay in their places).

@@ -105,6 +105,9 @@ struct MassCursor {
 // kFresh the position is the accepted token at `place`, seen from there on. (As
 // a condition in one function the places' loads and comparisons were issued for
 // every position, 4 of 9.5 instructions a score.)
+// A weight that is zero (a token that does not see the place, -lse = -infinity of
+// a row that is none) adds nothing: the MUFU gives 0, the polynomial what fadd2_ftz
+// takes as 0. So do weights below 2^-126, wherever their row falls.
 template <int N, bool kFresh>
 __device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* nlse, const int16_t* tok, float sl2, int place,
                                          float (&sum)[8]) {
@@ -129,8 +132,8 @@ __device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* nl
       }
     }
     const int s = (4 * i) & 7;
-    fadd2(sum[s], sum[s + 1], sum[s], sum[s + 1], y[0], y[1]);
-    fadd2(sum[s + 2], sum[s + 3], sum[s + 2], sum[s + 3], y[2], y[3]);
+    fadd2_ftz(sum[s], sum[s + 1], sum[s], sum[s + 1], y[0], y[1]);
+    fadd2_ftz(sum[s + 2], sum[s + 3], sum[s + 2], sum[s + 3], y[2], y[3]);
   }
 }
 

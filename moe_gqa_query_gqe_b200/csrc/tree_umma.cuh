@@ -177,14 +177,17 @@ struct TuCursor {
   }
 };
 
-// 2^x for a pair on the FMA pipe, to 4e-6: as exp2_poly2 of attn2.cuh with a
-// polynomial of degree 4 (fit_exp2_poly.py), for the log-sum in fp32 beside O.
+// 2^x for a pair on the FMA pipe, to 2.7e-6 relative for -126 < x < 128: as
+// exp2_poly2 of attn2.cuh with a polynomial of degree 4 (fit_exp2_poly.py), for
+// the log-sum in fp32 beside O. From -126 down (-infinity too) the result is a
+// subnormal number, 2^-126 / sqrt(2) at least: nothing to a softmax, whose largest term is
+// near 1, and zero once added with fadd2_ftz. Not for x >= 128, nor for NaN.
 __device__ __forceinline__ void exp2_poly4(float& y0, float& y1, float x0, float x1) {
   constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
   constexpr float c0 = 9.999992847e-01f, c1 = 6.931217909e-01f, c2 = 2.402474433e-01f, c3 = 5.591785908e-02f,
                   c4 = 9.570102207e-03f;
-  x0 = fmaxf(x0, -125.0f);
-  x1 = fmaxf(x1, -125.0f);
+  x0 = fmaxf(x0, -126.5f);  // (halfway to the even exponent -126, so that the bits below stay positive)
+  x1 = fmaxf(x1, -126.5f);
   float t0, t1, j0, j1, f0, f1, p0, p1;
   fadd2(t0, t1, x0, x1, kShift, kShift);
   fadd2(j0, j1, t0, t1, -kShift, -kShift);
@@ -195,6 +198,15 @@ __device__ __forceinline__ void exp2_poly4(float& y0, float& y1, float x0, float
   ffma2(p0, p1, p0, p1, f0, f1, c0, c0);
   y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
   y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+
+// Sums of a pair; subnormal terms and sums are zero.
+__device__ __forceinline__ void fadd2_ftz(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.ftz.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 constexpr int kTuPiece = 4;  // columns a thread finishes at a time

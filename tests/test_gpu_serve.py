@@ -529,6 +529,24 @@ def test_commit_path_index_out_of_range_adds_nothing(d, cap, lens, acc):
     assert gqe.gqe_check_error() == 0
 
 
+@pytest.mark.parametrize("d,cap,lens", [(Dims(B=2, T=9, D=64, G=4, M=2, k=1), 300, [280, 130]), (Dims(B=1, T=25, D=64, G=2, M=8, k=4), 700, [640]),
+                                        (Dims(B=1, T=128, D=64, G=1, M=8, k=8), 300, [129])], ids=["few", "many", "most"])
+def test_commit_weights_of_zero_add_nothing(d, cap, lens):
+    """e^-300 is no fp32 number, and a token does not see the places behind its
+    own: sums of such weights alone are exactly zero, whatever columns of the
+    products they fall in."""
+    x = commit_inputs(d, cap, lens, None, "none", 22)
+    far = dict(x, lse=torch.full_like(x["lse"], 300.0), mass=torch.zeros_like(x["mass"]))
+    mass = run_commit(d, cap, cu(far))[3]
+    last = dict(x, lse=x["lse"].clone(), mass=torch.zeros_like(x["mass"]))
+    last["lse"].view(d.B, d.T, -1)[:, -1] = 300.0
+    mass_last = run_commit(d, cap, cu(last))[3]
+    ok()
+    for b, L in enumerate(lens):
+        assert (mass[b, :, :L + d.T] == 0).all()
+        assert (mass_last[b, :, L + d.T - 1] == 0).all() and (mass_last[b, :, :L + d.T - 1] > 0).all()
+
+
 # ---- eviction ------------------------------------------------------------------------------
 EVICT = [
     (Dims(B=1, T=8, D=64, G=8, M=1, k=1), [8], 7, 1, 1),
