@@ -54,7 +54,7 @@ struct MassParams {
 };
 struct MassSmem {
   static constexpr int kLse = 0;                                // [1152] -lse, log2 units
-  static constexpr int kTok = kLse + kMassMaxRows * 4;          // [1152] place of the row's token in the path
+  static constexpr int kTok = kLse + kMassMaxRows * 4;          // [1152] place of the row's token in the path, -1: no token
   static constexpr int kOld = kTok + kMassMaxRows * 2;          // [4][256] sums so far
   static constexpr int kPrefix = kOld + 4096;                   // [B + 1]
   static constexpr int kBar = kPrefix + (kTreeMaxB + 1) * 8;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
           const float ls = tok >= 0 ? p.lse[qrow] * -1.4426950408889634f : -INFINITY;  // (no row: every weight is 0)
           if (ls != ls) s_nan[units & 1] = 1;  // (the polynomial would lose it)
           s_nlse[r] = ls;
-          s_tok[r] = (int16_t)max(j, 0);
+          s_tok[r] = (int16_t)(tok >= 0 ? j : -1);
         }
       }
       fence_proxy_async_smem();
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
         if (row < valid) {
           float w = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
           // a place whose path index is out of range holds no token (its key here is zero)
-          if (fresh && commit_token(p, it.b, row) < 0) w = 0.f;
+          if (fresh && s_tok[row * p.k] < 0) w = 0.f;
           p.mass_out[at + s0 + row] = old + w;
         }
       }
