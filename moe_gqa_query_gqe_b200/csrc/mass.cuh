@@ -124,7 +124,7 @@ __device__ __forceinline__ void mass_add(const uint32_t (&a)[N], const float* nl
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if ((2 * i + e) % kMassPolyEvery == kMassPolyEvery - 1) {
+      if (!kFresh && (2 * i + e) % kMassPolyEvery == kMassPolyEvery - 1) {
         exp2_poly4(y[2 * e], y[2 * e + 1], x[2 * e], x[2 * e + 1]);
       } else {
         y[2 * e] = ex2_approx(x[2 * e]);
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
   uint64_t* s_free = s_full + 4;                                   // [2][2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_free + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* s_nan = reinterpret_cast<int*>(tmem_slot + 2);              // [2] units: a row's lse is NaN
+  int* s_nan = reinterpret_cast<int*>(tmem_slot + 2);              // [2] units: a row's weights are NaN
   float* s_nlse = reinterpret_cast<float*>(smem + S::kLse);
   float* s_old = reinterpret_cast<float*>(smem + S::kOld);
   int16_t* s_tok = reinterpret_cast<int16_t*>(smem + S::kTok);
@@ -351,7 +351,9 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
         *reinterpret_cast<uint4*>(smem + S::kQ + (r >> 7) * 16384 + (r & 127) * 128 + ((ch ^ (r & 7)) << 4)) = v;
         if (ch == 0) {
           const float ls = tok >= 0 ? p.lse[qrow] * -1.4426950408889634f : -INFINITY;  // (no row: every weight is 0)
-          if (ls != ls) s_nan[units & 1] = 1;  // (the polynomial would lose it)
+          // NaN, or +infinity where all of the row's scores are -infinity: every
+          // cached position's sum is NaN (the polynomial would lose it)
+          if (!(ls < INFINITY)) s_nan[units & 1] = 1;
           s_nlse[r] = ls;
           s_tok[r] = (int16_t)(tok >= 0 ? j : -1);
         }
@@ -388,7 +390,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) cache_mass_kernel(const __gri
         asm volatile("cp.async.wait_group 3;" ::: "memory");
         const float old = s_old[(slot & 3) * 256 + wtid];
         ++slot;
-        float sum[8] = {nan, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        // (of the accepted rows only those that its token sees: MUFU, which keeps it)
+        float sum[8] = {fresh ? 0.f : nan, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int r0 = 0; r0 < it.R; r0 += 128, ++s_cnt) {
           const int buf = s_cnt & 1;
           w_ok = mbar_wait(&s_full[t * 2 + buf], (s_cnt >> 1) & 1, abort_flag);

@@ -547,6 +547,32 @@ def test_commit_weights_of_zero_add_nothing(d, cap, lens):
         assert (mass_last[b, :, L + d.T - 1] == 0).all() and (mass_last[b, :, :L + d.T - 1] > 0).all()
 
 
+@pytest.mark.parametrize("value", [NAN, -float("inf")])
+@pytest.mark.parametrize("d,cap,L,n", [(Dims(B=1, T=12, D=64, G=4, M=2, k=1), 300, 200, 10), (Dims(B=1, T=60, D=64, G=2, M=8, k=4), 500, 300, 60)],
+                         ids=["few", "many"])
+def test_commit_weights_that_are_not_numbers_reach_what_their_token_sees(d, cap, L, n, value):
+    """A log-sum of NaN, or of -infinity (all of its scores are -infinity), makes
+    NaN of the group's cached sums and of those up to the token's own place; the
+    places behind, which the token does not see, keep theirs."""
+    x = commit_inputs(d, cap, [L], [n], "path", 23)
+    for j in (0, 1, n // 2, n - 2, n - 1):
+        for slot in (0, d.k, d.G * d.k):  # of group 0, group 1, and the shared head of group 0
+            y = dict(x, lse=x["lse"].clone(), Q=x["Q"].clone(), Kc=x["Kc"].abs(), Kn=x["Kn"].abs())
+            base = run_commit(d, cap, cu(y))[3]
+            tok = int(x["path"][0, j])
+            y["lse"][tok, slot] = value
+            if value == -float("inf"):
+                y["Q"][tok, slot] = 0
+                y["Q"][tok, slot, 5] = -float("inf")  # (keys are not negative here)
+            mass = run_commit(d, cap, cu(y))[3]
+            want = torch.zeros_like(mass, dtype=torch.bool)
+            want[0, 1 if slot == d.k else 0, :L + j + 1] = True
+            assert torch.equal(mass.isnan() & ~base.isnan(), want & ~base.isnan()), (j, slot)
+            rest = ~(want | base.isnan())
+            assert torch.equal(mass[rest], base[rest]), (j, slot)
+    ok()
+
+
 # ---- eviction ------------------------------------------------------------------------------
 EVICT = [
     (Dims(B=1, T=8, D=64, G=8, M=1, k=1), [8], 7, 1, 1),
