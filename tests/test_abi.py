@@ -128,3 +128,16 @@ def test_valid_call_without_a_device_reports_no_device():
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device answer")
 def test_wait_self_test_without_a_device_reports_no_device():
     assert _raw("gqe_selftest_wait_timeout", None) == -6
+
+
+def test_dimensions_of_any_number_type():
+    """Whatever int() takes is a dimension, in a dict as in an object."""
+    import numpy as np
+    plain = dict(B=2, T=64, D=256, G=4, M=2, k=1, dh=64)
+    want = bytes(lib.dims_struct(plain))
+    for kind in (float, np.int64, np.float32, torch.tensor, str):
+        d = {key: kind(v) for key, v in plain.items()}
+        assert bytes(lib.dims_struct(d)) == want
+        assert lib.workspace_bytes(d, gqe.OP_TREE_ATTN) == lib.workspace_bytes(plain, gqe.OP_TREE_ATTN) > 0
+    for d in (type("Kind", (dict,), {})(plain), Dims(**{key: plain[key] for key in ("B", "T", "D", "G", "M", "k")})):
+        assert bytes(lib.dims_struct(d)) == want
