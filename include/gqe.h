@@ -418,6 +418,8 @@ int gqe_qk_rope(const gqe_dims* d, int layout, int rot, float eps, float scale,
  *      over the attended rows, or NULL. Rows i >= draft_len[b] are left as they
  *      were.
  * What a masked row holds never reaches a result, infinities and NaN included.
+ * An attended value that is infinite or NaN makes its column so, as the formula
+ * does (NaN where an infinite one's weight underflows).
  * Arithmetic: S, l and O accumulate in fp32, P rounded to bf16 before P V.
  * ws : gqe_workspace_bytes(d, GQE_OP_TREE_ATTN); it does not grow with cap.
  * No atomics: the same call gives the same bits. The keys are cut into ranges by

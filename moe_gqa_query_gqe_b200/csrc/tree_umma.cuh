@@ -243,6 +243,19 @@ __device__ __forceinline__ TuItem tu_item(const TuWarp* w) {  // read anew at ev
   return it;
 }
 
+// The sum of the values in column c of an item's cached rows that are not finite;
+// `none` where there are none. Rarely called, and slow.
+__device__ __noinline__ float tu_not_finite(const TreeParams& p, const TuItem& it, int c, float none) {
+  const __nv_bfloat16* v = p.Vc + ((size_t)it.b * p.cap * p.G + it.g) * 64 + c;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int s = it.j0 * kTuBlock; s < min(it.L, it.j1 * kTuBlock); ++s) {
+    const float x = __bfloat162float(v[(size_t)s * p.G * 64]);
+    if (!isfinite(x)) sum += x;
+  }
+  return sum == 0.f ? none : sum;
+}
+
 // The barriers and tensor-memory addresses of one tile's softmax warps.
 struct TuTile {
   uint64_t *s_free, *pv_done, *p_full;
@@ -889,6 +902,15 @@ __global__ void __launch_bounds__(kTuThreads, 1) tree_attn_umma_kernel(const __g
             o[2] += a.z;
             o[3] += a.w;
           }
+        }
+        if (D > 1 && live && l == l) {
+          // Zeros of the other copy's keys times a cached value that is infinite are
+          // NaN. The row's weights are numbers, so that its sums are too but for such
+          // values, and those alone decide: their sum (0 x infinity is the weight's only
+          // where it underflows).
+#pragma unroll
+          for (int i = 0; i < kTuPiece; ++i)
+            if (o[i] != o[i]) o[i] = tu_not_finite(p, it, c + i, o[i]);
         }
         if (any_bad && live) {
           for (int w = 0; w < 4; ++w)

@@ -319,6 +319,37 @@ def test_tree_values_that_are_not_finite_reach_descendants_only(k, T, large):
     assert np.isnan(lse[sees[:, 8]][:, g0]).all() and np.array_equal(lse[:, g1], lsec[:, g1])
 
 
+@pytest.mark.parametrize("large", [False, True])
+@pytest.mark.parametrize("T,k,lens", [(12, 1, [70]), (17, 2, [128, 3]), (34, 1, [5000, 129]), (64, 1, [300]), (100, 1, [257]), (128, 2, [90])])
+def test_tree_cached_values_that_are_not_finite(T, k, lens, large):
+    """Every token attends the cached rows: an infinite value is infinite in its
+    column of the group's rows, one of either sign or a NaN is NaN, and the other columns
+    are what they would be (in both kernels, whatever rows share a tile)."""
+    d = Dims(B=len(lens), T=T, D=64, G=2, M=4, k=k)
+    x = tree_inputs(d, max(lens) + 2, lens, None, "tree", 9)
+    for b, L in enumerate(lens):
+        V = x["Vc"][b]
+        V[0, 1, 3], V[L - 1, 1, 4], V[L // 2, 1, 63] = float("inf"), -float("inf"), NAN
+        V[0, 1, 17], V[L - 1, 1, 17] = float("inf"), -float("inf")
+        V[L // 3, 0, 0] = float("inf")
+        V[:L, 0, 40] = -float("inf")
+    x["Vn"][2, 1, 3], x["Vn"][3, 1, 4] = float("inf"), float("inf")  # drafted values of the same columns
+    cap = max(large_capacity(d), max(lens) + 2) if large else max(lens) + 2
+    O, lse = run_tree(d, cap, cu(roomier(x, cap)))
+    ok()
+    with np.errstate(invalid="ignore"):
+        want = ref.tree_attn(x["Q"], x["Kn"], x["Vn"], x["Kc"], x["Vc"], lens, None, x["parent"].numpy(), d.B, d.T, d.G, d.k)
+    got = f64(O)
+    for kind in (np.isnan, np.isposinf, np.isneginf):
+        assert kind(want["O"]).any()
+        np.testing.assert_array_equal(kind(got), kind(want["O"]))
+    fine = np.isfinite(want["O"])
+    s = 2.0 ** -17 * want["score"]
+    tol = HALF * (np.abs(want["O"]) + want["terms"]) + (2 * s + 2.0 ** -14)[..., None] * want["terms"]
+    within(got[fine], want["O"][fine], tol[fine], "O")
+    within(lse, want["lse"], s + 2.0 ** -20 * (1 + np.abs(want["lse"])), "lse")
+
+
 @pytest.mark.parametrize("T", [4, 40])
 def test_tree_extreme_scores(T):
     """Scores of several thousand either way: the softmax is a choice of one key."""
