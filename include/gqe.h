@@ -449,7 +449,9 @@ int gqe_tree_attn(const gqe_dims* d, int32_t cap, const void* Q,
  * counts it all the same (the rows behind it stay in their places).
  *
  * In : path [B, T] int32 in [0, T), or NULL: 0, 1, 2, ...; n_acc [B] int32 in
- *      [0, T], or NULL: T each; L + n <= cap;
+ *      [0, T], or NULL: T each; L + n <= cap; both name tokens below the
+ *      attention call's draft_len (of others Q, K_new, V_new and lse are whatever
+ *      the buffers hold);
  *      positions [B*T] int32 of the drafted tokens, or NULL: row L + j is at
  *      position L + j; Q, K_new, V_new and lse of the gqe_tree_attn call;
  *      cache_len [B] int32.

@@ -63,7 +63,9 @@ TreePlan tree_plan(const gqe_dims* d, bool umma) {
     t.step = R0 <= 128 ? d->G : 1;
     t.blocks = kTreeSms / t.step * t.step;
   } else {
-    // as many ranges as four blocks an SM allow, one wave
+    // as many ranges as four blocks an SM allow: one wave up to 32 rows. Of the
+    // variant for more (wr = 4, 168 registers) an SM holds three blocks, and up to a
+    // quarter of the ranges run after the others.
     t.step = per_seq;
     t.blocks = std::max(1, kTreeSms * 4 / per_seq) * per_seq;
   }

@@ -293,6 +293,40 @@ def test_tree_long_caches_match_the_formula(B, T, k, lens):
                 within(lse[rows, h], f64(ls), f64(size[:, 0]) + 2.0 ** -14 + 2.0 ** -20 * (1 + np.abs(f64(ls))), f"lse {b} {h}")
 
 
+@pytest.mark.parametrize("B,T,G,k,lens", [(1, 64, 4, 1, [14001]), (2, 33, 4, 1, [15000, 1023]), (3, 60, 2, 2, [9000, 0, 2111]), (1, 128, 1, 8, [9999]),
+                                          (1, 40, 64, 1, [5001])])
+def test_tree_many_rows_over_cut_caches_match_the_formula(B, T, G, k, lens):
+    """More than 32 rows a group over caches below the other kernel's 20 million
+    scores, in blocks of 64 rows whose keys are cut into ranges."""
+    d = Dims(B=B, T=T, D=64, G=G, M=max(k, 8 // G), k=k)
+    cap = max(lens) + 3
+    assert T * k > 32 and T * k * G * B * cap < 20_000_000
+    x = tree_inputs(d, cap, lens, None, "tree", 14)
+    v = cu(x)
+    O, lse = run_tree(d, cap, v)
+    O2, lse2 = run_tree(d, cap, v)
+    ok()
+    assert torch.equal(O2, O) and torch.equal(lse2, lse)
+    for b, L in enumerate(lens):
+        rows = slice(b * T, (b + 1) * T)
+        hidden = ~torch.from_numpy(ref.ancestors(x["parent"].numpy().reshape(B, T)[b], T)).cuda()
+        for g in range(0, G, max(1, G // 4)):
+            K = torch.cat([v["Kc"][b, :L, g], v["Kn"][rows, g]]).double()
+            V = torch.cat([v["Vc"][b, :L, g], v["Vn"][rows, g]]).double()
+            for h in ref.group_slots(g, G, k):
+                q = v["Q"][rows, h].double()
+                s = q @ K.T / 8.0
+                s[:, L:][hidden] = -float("inf")
+                p = torch.softmax(s, 1)
+                size = (q.abs() @ K.abs().T).amax(1, keepdim=True) / 8.0 * 2.0 ** -17
+                terms, want = p @ V.abs(), p @ V
+                # l adds up to 15 thousand terms in fp32, 2^-24 a step along chains of at most 16 a thread and 2^8 blocks
+                tol = HALF * (want.abs() + terms) + (2 * size + 2.0 ** -13) * terms
+                within(O[rows, h], f64(want), f64(tol), f"O {b} {h}")
+                ls = torch.logsumexp(s, 1)
+                within(lse[rows, h], f64(ls), f64(size[:, 0]) + 2.0 ** -14 + 2.0 ** -20 * (1 + np.abs(f64(ls))), f"lse {b} {h}")
+
+
 @pytest.mark.parametrize("k,T,large", [(1, 12, False), (4, 40, False), (4, 40, True), (1, 50, True)])
 def test_tree_values_that_are_not_finite_reach_descendants_only(k, T, large):
     d = Dims(B=1, T=T, D=64, G=2, M=4, k=k)
