@@ -940,6 +940,43 @@ def test_two_streams_with_workspaces_of_their_own():
     ok()
 
 
+def test_two_streams_of_commits_and_evictions():
+    """Calls at once on buffers of their own, in place and call after call, give
+    what they give one by one."""
+    d, cap, keep = Dims(B=3, T=8, D=64, G=8, M=2, k=1), 6000, 3000
+    dc = d.with_(T=cap)
+
+    def state(seed):
+        x = cu(commit_inputs(d, cap, [5000, 3100, 800], [8, 0, 3], "path", seed))
+        x["pos"] = torch.arange(cap, dtype=torch.int32, device="cuda").expand(d.B, d.G, cap).contiguous()
+        x.update(n1=torch.empty_like(x["lens"]), n2=torch.empty_like(x["lens"]), nxt=i32([6000] * 3).cuda(), ws=gqe.workspace(dc, gqe.OP_CACHE_EVICT))
+        return x
+
+    def steps(x, stream):
+        at, to = x["lens"], x["n1"]
+        for _ in range(4):
+            gqe.gqe_tree_commit(d, cap, x["path"], x["acc"], x["positions"], x["Q"], x["lse"], x["Kn"], x["Vn"], at, x["Kc"], x["Vc"], x["pos"],
+                                x["mass"], x["mass"], to, stream=stream)
+            gqe.gqe_cache_evict(dc, keep, 4, 100, to, x["nxt"], x["Kc"], x["Vc"], x["mass"], x["mass"], x["pos"], x["pos"], x["n2"], x["ws"], stream=stream)
+            at, to = x["n2"], x["n1"]
+
+    want = [state(s) for s in (61, 62)]
+    for x in want:
+        steps(x, None)
+        torch.cuda.synchronize()
+    got, streams = [state(s) for s in (61, 62)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for x, s in zip(got, streams):
+        steps(x, s)
+    torch.cuda.synchronize()
+    ok()
+    for x, w in zip(got, want):
+        assert w["n2"].tolist() == [3000, 3000, 812] and torch.equal(x["n2"], w["n2"])
+        for b, n in enumerate(w["n2"].tolist()):
+            assert torch.equal(x["mass"][b, :, :n], w["mass"][b, :, :n]) and torch.equal(x["pos"][b, :, :n], w["pos"][b, :, :n])
+            assert torch.equal(x["Kc"][b, :n], w["Kc"][b, :n]) and torch.equal(x["Vc"][b, :n], w["Vc"][b, :n])
+
+
 def test_tensors_of_another_kind_are_refused():
     d, cap = Dims(B=2, T=4, D=64, G=4, M=2, k=1), 50
     v = cu(tree_inputs(d, cap, [10, 20], None, "tree", 1))
