@@ -15,14 +15,15 @@
 // Bounds: 128 bytes of K and 8 of mass a position; one exponential a (row,
 // position), 16 a clock and SM on the MUFU, so that past about 90 rows the
 // exponentials bind; one pair in kMassPolyEvery is evaluated on the FMA pipe.
-// Measured, 8 groups: 8 x 6 accepted (one row a token) over 20001 to 32767
-// positions 44.3 us = 4.7 TB/s of 6.5 that a copy reaches; 2 x 128 (two rows)
-// over 60000 to 65536 130 us against 63 of exponentials on the MUFU alone: issue
-// and latency. Sixteen softmax warps took 118 us there, but 58-60 instead of 50
+// Measured, 8 groups: 8 x 6 accepted (one row a token; in one of the sequences
+// none) over 20001 to 32767 positions 41.9 us = 4.9 TB/s of 6.5 that a copy reaches;
+// 2 x 128 (two rows) over 60000 to 65536 128 us against 63 of exponentials on the
+// MUFU alone: issue and latency. Sixteen softmax warps took 118 us there, but 58-60 instead of 50
 // for 8 x 1 over 32767.
-// Work is cut as in tree_umma.cuh: ranges of equal weight over all positions,
-// one block per SM; with few rows the groups side by side, so that a
-// position's contiguous G rows are read at about the same time.
+// Work is cut as in tree_umma.cuh: ranges of equal weight over all positions of
+// the sequences that accept anything, one block per SM; up to 90 rows the groups side by
+// side, so that a position's contiguous G rows are read at about the same time (with
+// G = 32 or 64 on a multiple of G blocks, 128), above that one after the other.
 //
 //   warp 0      K blocks: the cache's by TMA; the accepted rows, the last block of
 //               a unit, gathered
@@ -43,6 +44,8 @@ namespace gqe {
 constexpr int kMassThreads = 384;
 constexpr int kMassMaxStages = 8;  // of K; an even number is used, so that a stage's blocks are all one tile's
 constexpr int kMassMaxRows = kTreeMax * 9;  // T * (k + 1)
+// The polynomial is off by 2.7e-6 at most, the MUFU by 2e-7; the exponent itself,
+// a difference of numbers between 8 and 32 in fp32, puts either off by 1e-6.
 constexpr int kMassPolyEvery = 4;
 
 struct MassParams {

@@ -32,8 +32,10 @@
 //
 // Measured, Q and K of 8 groups: 1 x 131072 tokens of 25 heads 171-177 us =
 // 4.8-5.0 TB/s of 6.5 that a copy reaches (265 us with loads through registers
-// and each thread its own angles); 8 x 2048 of 17 heads 18.6 us, of which 8 are
-// the start and the end of a short kernel; one token 2.3 us.
+// and each thread its own angles); 8 x 2048 of 17 heads 18.6 us: 14.8 at
+// the long case's rate, the rest the start and the end of a short kernel; one
+// token 2.3 us. In the interleaved layout a lane's two chunks are neighbours, so
+// that each of its stores covers every second 16 bytes of the head.
 #pragma once
 
 #include "attn2.cuh"

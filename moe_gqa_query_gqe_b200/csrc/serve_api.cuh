@@ -59,7 +59,7 @@ TreePlan tree_plan(const gqe_dims* d, bool umma) {
   t.units = (long long)d->B * per_seq;
   if (umma) {
     // the groups side by side where every group is one tile; else ranges over
-    // all units, whose weights differ
+    // all units, whose weights differ. (148 / G * G blocks: 128 with G = 32 or 64)
     t.step = R0 <= 128 ? d->G : 1;
     t.blocks = kTreeSms / t.step * t.step;
   } else {

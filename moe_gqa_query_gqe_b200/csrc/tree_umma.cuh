@@ -35,10 +35,13 @@
 // Bounds: one exponential a (row, position), 16 a clock and SM on the MUFU (one
 // pair in kTuPolyEvery on the FMA pipe), against 256 flops: 4 x 128 tokens of two
 // rows a group over 131072 positions of 8 groups take 253 us for the exponentials,
-// 179 for the products and 164 for the bytes. Measured there: 476 us (615
-// TFLOP/s) call after call on the same inputs, 529 over several sets in turn. The
+// 179 for the products and 164 for the bytes. Measured there: 531 us (550
+// TFLOP/s) over several sets of inputs in turn, 476 on one set again and again. The
 // two softmax warps of a scheduler wait for their own chains (issue slots 30-35%
-// used, MUFU 54% of the time). Sixteen warps, a row over four threads, took
+// used, MUFU 54% of the time): a block's scores are read in three steps, and S is
+// held until half of its exponentials are done. (attn2.cuh, with as many warps and
+// registers, holds all 128 scores of a row and spills 8 bytes; here the loop's
+// pointers and its masked forms take that room.) Sixteen warps, a row over four threads, took
 // 821-855 us (96 registers a thread spill); the next scores loaded from tensor
 // memory during a block's exponentials, in pieces of 32, 525 against 479 (88 bytes
 // a thread spill).
